@@ -32,7 +32,8 @@ EXPORTS = ["opq_quantize", "opq_dequantize", "opq_linear_workspace_size", "opq_l
            "opq_linear_grouped", "opq_linear_grouped_workspace_size", "opq_linear_fused",
            "opq_linear_grouped_fused", "opq_alpha_search", "opq_alpha_search_workspace_size",
            "opq_quantize_bits", "opq_dequantize_bits", "opq_set_wait_limit_ns",
-           "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size", "opq_dequantize_batched"]
+           "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size", "opq_dequantize_batched",
+           "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_cache_write", "opq_fp8_cache_read"]
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2}
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -79,6 +80,10 @@ def load(path: str = LIB_PATH):
     lib.opq_dequantize_batched.argtypes = [P, I, F, P]
     lib.opq_linear_bits.argtypes = [P, I, I, P, P, P, I, ctypes.c_int32, F, P, P, S, P]
     lib.opq_linear_bits_workspace_size.argtypes = [I, I, I, ctypes.c_int32, ctypes.POINTER(S)]
+    lib.opq_fp8_quantize.argtypes = [P, ctypes.c_int32, I, I, I, I, P, I, P, I, P]
+    lib.opq_fp8_linear.argtypes = [P, I, P, I, I, I, P, I, P, I, I, P, ctypes.c_int32, P, ctypes.c_int32, I, P]
+    lib.opq_fp8_cache_write.argtypes = [P, P, ctypes.c_int32, I, I, I, ctypes.c_int32, I, P, P]
+    lib.opq_fp8_cache_read.argtypes = [P, P, ctypes.c_int32, I, I, I, ctypes.c_int32, I, P, I, P, I, I, P, P]
     lib.opq_status_string.argtypes = [ctypes.c_int]
     lib.opq_status_string.restype = ctypes.c_char_p
     for f in ("opq_quantize", "opq_dequantize", "opq_linear_workspace_size", "opq_linear", "opq_linear_plan",
@@ -86,7 +91,8 @@ def load(path: str = LIB_PATH):
               "opq_linear_grouped_workspace_size", "opq_linear_fused", "opq_linear_grouped_fused",
               "opq_alpha_search", "opq_alpha_search_workspace_size", "opq_quantize_bits", "opq_dequantize_bits",
               "opq_set_wait_limit_ns", "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size",
-              "opq_dequantize_batched"):
+              "opq_dequantize_batched", "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_cache_write",
+              "opq_fp8_cache_read"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -434,6 +440,7 @@ def linear_noalloc(x: torch.Tensor, codes: torch.Tensor, signs: torch.Tensor, sc
 
 DEVERR_WAIT_TIMEOUT = 1
 DEVERR_SMEM_ALIGN = 2
+DEVERR_INDEX = 4
 
 
 def device_error(device=None) -> int:
@@ -446,3 +453,6 @@ def device_error(device=None) -> int:
 def set_wait_limit_ns(ns: int = 0):
     """Time after which the kernels' bounded waits give up on the current device (0: the 4 s default)."""
     _check(load().opq_set_wait_limit_ns(int(ns)), "opq_set_wait_limit_ns")
+
+
+from .fp8 import fp8_cache_read, fp8_cache_write, fp8_linear, fp8_quantize  # noqa: E402

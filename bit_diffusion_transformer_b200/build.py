@@ -1,4 +1,4 @@
-"""Build libopq.so (the whole CUDA library is one translation unit) for sm_100a, in-tree."""
+"""Build libopq.so (two translation units, compiled side by side) for sm_100a, in-tree."""
 from __future__ import annotations
 
 import os
@@ -10,9 +10,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(HERE, "libopq.so")
-SOURCES = ["opq_capi.cu"]
+SOURCES = ["opq_capi.cu", "opq_fp8.cu"]
 HEADERS = ["opq_bits.h", "opq_device.cuh", "opq_quantize.cuh", "opq_quantize_stream.cuh", "opq_dequantize.cuh",
-           "opq_linear.cuh", "opq_linear_wide.cuh", "opq_grouped.cuh"]
+           "opq_linear.cuh", "opq_linear_wide.cuh", "opq_grouped.cuh", "opq_host.h", "opq_fp8_format.cuh",
+           "opq_fp8_quantize.cuh", "opq_fp8_cache.cuh", "opq_fp8_linear.cuh"]
 
 
 def _nvcc() -> str:
@@ -34,12 +35,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return SO
     tmp = SO + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC, "-o", tmp,
-           os.path.join(CSRC, "opq_capi.cu")]
+    flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
+             "-I", INCLUDE, "-I", CSRC]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
+        flags.append("-Xptxas=-v")
+    objs = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    try:
+        jobs = [subprocess.Popen([_nvcc(), *flags, "-c", os.path.join(CSRC, src), "-o", obj])
+                for src, obj in zip(SOURCES, objs)]
+        codes = [j.wait() for j in jobs]
+        if any(codes):
+            raise subprocess.CalledProcessError(max(codes), "nvcc")
+        subprocess.check_call([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs])
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, SO)
     return SO
 

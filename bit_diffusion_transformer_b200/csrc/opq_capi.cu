@@ -14,6 +14,7 @@
 #include "opq.h"
 #include "opq_dequantize.cuh"
 #include "opq_grouped.cuh"
+#include "opq_host.h"
 #include "opq_linear.cuh"
 #include "opq_linear_wide.cuh"
 #include "opq_quantize.cuh"
@@ -32,14 +33,7 @@ opq_status cuda_fail(cudaError_t e) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Tensor pointers: all non-null and 16-byte aligned first, then each must be
-// device-accessible memory (device or managed), so that the cheapest argument
-// error is reported regardless of pointer order.
-opq_status check_ptrs(std::initializer_list<const void *> ptrs) {
-    for (const void *p : ptrs)
-        if (p == nullptr) return OPQ_ERR_INVALID_ARG;
-    for (const void *p : ptrs)
-        if (!aligned16(p)) return OPQ_ERR_MISALIGNED;
+opq_status check_device(std::initializer_list<const void *> ptrs) {
     for (const void *p : ptrs) {
         cudaPointerAttributes attr;
         cudaError_t e = cudaPointerGetAttributes(&attr, p);
@@ -50,6 +44,17 @@ opq_status check_ptrs(std::initializer_list<const void *> ptrs) {
         if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) return OPQ_ERR_NOT_DEVICE_MEMORY;
     }
     return OPQ_OK;
+}
+
+// Tensor pointers: all non-null and 16-byte aligned first, then each must be
+// device-accessible memory (device or managed), so that the cheapest argument
+// error is reported regardless of pointer order.
+opq_status check_ptrs(std::initializer_list<const void *> ptrs) {
+    for (const void *p : ptrs)
+        if (p == nullptr) return OPQ_ERR_INVALID_ARG;
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return OPQ_ERR_MISALIGNED;
+    return check_device(ptrs);
 }
 
 bool alpha_ok(float alpha) { return std::isfinite(alpha) && alpha > 0.0f; }
@@ -385,6 +390,17 @@ cudaError_t launch_linear_wide(DeviceInfo *di, const Plan &plan, const CUtensorM
 }
 
 }  // namespace
+
+// the helpers that opq_fp8.cu shares (opq_host.h)
+namespace opqhost {
+opq_status cuda_fail(int code) {
+    t_last_cuda_error = code;
+    return OPQ_ERR_CUDA;
+}
+opq_status check_ptrs(std::initializer_list<const void *> ptrs) { return ::check_ptrs(ptrs); }
+opq_status check_device(std::initializer_list<const void *> ptrs) { return ::check_device(ptrs); }
+EncodeTiledFn encode_fn() { return ::encode_fn(); }
+}  // namespace opqhost
 
 extern "C" {
 
@@ -1072,6 +1088,9 @@ extern "C" opq_status opq_device_error(void *stream, uint32_t *err) {
     if (e != cudaSuccess) return cuda_fail(e);
     e = cudaMemcpyToSymbol(opqdev::g_error, &zero, sizeof zero);
     if (e != cudaSuccess) return cuda_fail(e);
+    uint32_t v8 = 0;
+    e = opqhost::fp8_device_error(&v8);
+    if (e != cudaSuccess) return cuda_fail(e);
     if (v & opqdev::kErrWaitTimeout) {
         // A call that gave up waiting can leave arrival counters or published flags set. In a
         // caller's workspace the caller zeroes them; the allocation-free linear's counters sit
@@ -1091,13 +1110,14 @@ extern "C" opq_status opq_device_error(void *stream, uint32_t *err) {
             if (e != cudaSuccess) return cuda_fail(e);
         }
     }
-    *err = v;
+    *err = v | v8;
     return OPQ_OK;
 }
 
 extern "C" opq_status opq_set_wait_limit_ns(uint64_t ns) {
     const uint64_t v = ns == 0 ? opqdev::kWaitLimitNs : ns;
     cudaError_t e = cudaMemcpyToSymbol(opqdev::g_wait_limit_ns, &v, sizeof v);
+    if (e == cudaSuccess) e = opqhost::fp8_set_wait_limit(v);
     return e == cudaSuccess ? OPQ_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,161 @@
+// opq_fp8_format.cuh — the 8-bit block format: e4m3 codes (4 exponent bits, 3 mantissa bits,
+// largest value 448) with one fp32 scale per block of up to 128 values.
+//
+//   m     = max(largest finite |x| of the block, 2^-64)
+//   scale = fl32(m / 448)
+//   code  = the e4m3 number nearest 448 x / m, ties to even;  +-inf -> +-448, NaN -> NaN
+//   value = fl32(code * scale), rounded once more to the output's 16-bit type
+//
+// The code is exact for bf16 and fp16 inputs. 448 x / m is formed as y / a with y = (7/8) x and
+// a = m / 512, both exact in fp32 (at most 14 significant bits; a y that loses bits to fp32's
+// subnormal range is below 2^-50 of the block's largest and codes to 0 either way). The
+// correctly rounded fp32 quotient then rounds to the same e4m3 number as the real quotient: a
+// quotient that is not itself halfway between two codes differs from every such midpoint by at
+// least 2^-17 of its size (numerators of at most 14 bits, denominators of at most 11, midpoints
+// of 5), far more than fp32's 2^-24; and one that is halfway is an fp32 number, so it is
+// returned exactly and the conversion sees the tie.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace opqfp8 {
+
+constexpr int kBlock = 128;                       // values that share a scale along the row
+constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64
+
+enum { DT_BF16 = 0, DT_FP16 = 1 };
+
+// Per-block constants of the encoder.
+struct BlockScale {
+    float m, a, inv, scale;
+    __device__ __forceinline__ explicit BlockScale(float amax) {
+        m = fmaxf(amax, kFloor);
+        a = m * 0.001953125f;   // m / 512
+        inv = 1.0f / a;
+        scale = m / 448.0f;
+    }
+};
+
+// Two fp32 operands per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// Two fp32 values to e4m3, nearest even, magnitudes above 448 to 448, NaN kept: x in bits 0..7.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float2 v) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(v.y), "f"(v.x));
+    return d;
+}
+
+// Two e4m3 values (bits 0..7 and 8..15) to fp32, exact (through fp16, whose range and precision
+// contain e4m3's).
+__device__ __forceinline__ float2 decode_e4m3x2(uint16_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+template <int DT>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+    if (DT == DT_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float2 v) {
+    uint32_t d;
+    if (DT == DT_BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(v.y), "f"(v.x));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(v.y), "f"(v.x));
+    return d;
+}
+// One fp32 value rounded to the 16-bit type.
+template <int DT>
+__device__ __forceinline__ uint16_t pack16_1(float v) {
+    return (uint16_t)pack16<DT>(make_float2(v, 0.0f));
+}
+template <int DT>
+__device__ __forceinline__ float unpack16_1(uint16_t v) {
+    return DT == DT_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+}
+
+// The largest magnitude's bits of eight 16-bit values: magnitudes order as integers, and a
+// result at or above kInfBits says that the eight hold an infinity or a NaN.
+template <int DT>
+constexpr uint32_t kInfBits = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
+
+__device__ __forceinline__ uint32_t absmax8(const uint4 &v) {
+    const uint32_t k = 0x7FFF7FFFu;
+    const uint32_t w = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+    return max(w & 0xFFFFu, w >> 16);
+}
+// The same over the finite values only (the rare block that holds an infinity or a NaN).
+template <int DT>
+__device__ __forceinline__ uint32_t absmax8_finite(const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+        if (lo < kInfBits<DT>) best = max(best, lo);
+        if (hi < kInfBits<DT>) best = max(best, hi);
+    }
+    return best;
+}
+template <int DT>
+__device__ __forceinline__ float bits_to_float(uint32_t b) {
+    return unpack16_1<DT>((uint16_t)b);
+}
+
+// Eight values to eight codes. `clamp` (a block with non-finite values) takes infinities to +-m
+// first, keeping NaN; finite values are never above m.
+template <int DT>
+__device__ __forceinline__ uint2 encode8(const uint4 &v, const BlockScale &s, bool clamp) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+    const float2 inv = make_float2(s.inv, s.inv), na = make_float2(-s.a, -s.a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 x = unpack16<DT>(w[i]);
+        if (clamp) {
+            x.x = x.x > s.m ? s.m : (x.x < -s.m ? -s.m : x.x);
+            x.y = x.y > s.m ? s.m : (x.y < -s.m ? -s.m : x.y);
+        }
+        const float2 y = mul2(x, make_float2(0.875f, 0.875f));
+        float2 q = mul2(y, inv);                       // within an ulp or two of y / a
+        q = fma2(fma2(q, na, y), inv, q);              // the residual is exact: correctly rounded
+        c[i] = cvt_e4m3x2(q);
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// n / d and n % d for n < 2^31 by a multiplication (d is fixed per launch).
+struct FastDiv {
+    uint32_t d, mul, shift;
+    __host__ static FastDiv make(uint32_t d) {
+        FastDiv f{};
+        f.d = d;
+        uint32_t s = 0;
+        while (((uint64_t)1 << s) < d) ++s;
+        f.mul = (uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d);   // d = 1: 2^31
+        f.shift = 31 + s;
+        return f;
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> shift); }
+};
+
+}  // namespace opqfp8

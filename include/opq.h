@@ -325,12 +325,115 @@ opq_status opq_linear_noalloc(const uint16_t *x, int64_t M, int64_t K, const uin
                               uint16_t *y, void *stream);
 
 /*
+ * The 8-bit block format — e4m3 codes (8-bit floating point, 4 exponent and 3 mantissa bits,
+ * largest value 448) with one fp32 scale per block of 128 values along the row, for products
+ * at the 8-bit tensor rate and for caches. Per block:
+ *     m     = max(largest finite |x|, 2^-64)
+ *     scale = fl32(m / 448)
+ *     code  = the e4m3 number nearest 448 x / m (ties to even); infinities -> +-448, NaN -> NaN
+ * and a code c stands for c * scale. The last block of a row is shorter where the row's length
+ * is not a multiple of 128. 16-bit tensors are bf16 or fp16 (`dtype`, OPQ_DTYPE_*), passed as
+ * their bit patterns.
+ *
+ * These calls need no workspace, may run at the same time on several streams and inside graph
+ * captures, and are deterministic: the same inputs give the same bits. Row strides are in
+ * elements. Tensors are 16-byte aligned except scales, slots and page tables, which need their
+ * element's alignment.
+ */
+#define OPQ_DTYPE_BF16 0
+#define OPQ_DTYPE_FP16 1
+
+/*
+ * opq_fp8_quantize — a 16-bit matrix to the 8-bit block format.
+ *   x           [R, ldx] device; columns 0..K-1 of each row; ldx >= K, ldx % 8 == 0; K % 32 == 0
+ *   block_rows  1: a scale per (row, 128 columns), for activations;
+ *               128: a scale per block of 128 x 128, for weights (the last blocks are smaller)
+ *   codes       [R, ldc] bytes, written; ldc >= K, ldc % 16 == 0
+ *   scales      [ceil(K / 128), lds] fp32, written: scales[b * lds + r / block_rows] is the scale
+ *               of row r, columns 128 b ..; lds >= ceil(R / block_rows)
+ * The codes are exact: the same as from real arithmetic on the 16-bit inputs.
+ */
+opq_status opq_fp8_quantize(const void *x, int32_t dtype, int64_t R, int64_t K, int64_t ldx, int64_t block_rows,
+                            uint8_t *codes, int64_t ldc, float *scales, int64_t lds, void *stream);
+
+/*
+ * opq_fp8_linear — y = act(x W^T + bias), both operands in the 8-bit block format:
+ *     y[m, n] = act(sum_b sx[b, m] sw[b, n / 128] (sum_{k in block b} xc[m, k] wc[n, k]) + bias[n])
+ *   x, x_scales      codes [M, ldx] and scales [ceil(K / 128), ld_xs] with block_rows = 1
+ *   w, w_scales      codes [N, ldw] and scales [ceil(K / 128), ld_ws] with block_rows = 128
+ *   bias             16-bit [N] of type dtype, or NULL for none
+ *   activation       OPQ_ACT_*, evaluated as by opq_linear_fused
+ *   y                16-bit [M, ldy] of type dtype, written; ldy >= N
+ * ldx, ldw >= K and multiples of 16; K % 32 == 0. The blocks' sums are formed by the tensor cores
+ * (fp32 accumulators), scaled and added in fp32 in a fixed order, and rounded once.
+ */
+opq_status opq_fp8_linear(const uint8_t *x, int64_t ldx, const float *x_scales, int64_t ld_xs, int64_t M, int64_t K,
+                          const uint8_t *w, int64_t ldw, const float *w_scales, int64_t ld_ws, int64_t N,
+                          const void *bias, int32_t activation, void *y, int32_t dtype, int64_t ldy, void *stream);
+
+/*
+ * A paged cache of keys or of values in the 8-bit block format: `pages` pages of `page_size`
+ * token slots, `heads` heads of head_dim channels each, blocks of 128 along a head's channels.
+ * The code of (page, slot, head, channel c) is at
+ *     codes  + page * page_stride + slot * token_stride + head * head_stride + c         (bytes)
+ *     scales + page * scale_page_stride + slot * scale_token_stride
+ *            + head * scale_head_stride + c / 128                                        (floats)
+ * so any order of the page's tokens and heads is served. Code strides are multiples of 16,
+ * head_dim is a multiple of 16; elements must not overlap.
+ */
+typedef struct opq_fp8_cache {
+    uint8_t *codes;
+    float *scales;
+    int64_t head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+} opq_fp8_cache;
+/* 16-bit rows [tokens][heads][head_dim], strides in elements (multiples of 8), channels contiguous */
+typedef struct opq_rows {
+    void *data;
+    int64_t token_stride, head_stride;
+} opq_rows;
+
+/*
+ * opq_fp8_cache_write — quantizes tokens' keys and values into their slots.
+ *   cache, rows   HOST arrays of `tensors` (1 or 2) caches and inputs, read before the call
+ *                 returns; rows[i] has the cache's heads and head_dim
+ *   slots         int64 [tokens] device: page * page_size + slot of each token. A negative entry
+ *                 (padding) is skipped. An entry at or past pages * page_size is skipped and
+ *                 recorded (OPQ_DEVERR_INDEX). Entries >= 0 must differ within a call: two
+ *                 tokens sent to one slot leave that slot (no other) with a mix of both.
+ * tokens = 0 does nothing.
+ */
+opq_status opq_fp8_cache_write(const opq_fp8_cache *cache, const opq_rows *rows, int32_t tensors, int64_t pages,
+                               int64_t page_size, int64_t heads, int32_t dtype, int64_t tokens, const int64_t *slots,
+                               void *stream);
+
+/*
+ * opq_fp8_cache_read — decodes a batch of sequences' cached tokens into packed rows.
+ *   cu_rows       int32 [seqs + 1] device, ascending: sequence b's tokens go to output rows
+ *                 cu_rows[b] .. cu_rows[b + 1] - 1 (an empty range is fine)
+ *   starts        int32 [seqs] device, the position in the sequence of its first row, or NULL for 0
+ *   page_table    int32 [seqs, ld_table] device, table_width pages listed per sequence: the token
+ *                 at position p is in page page_table[b, p / page_size], slot p % page_size
+ *   rows          HOST array of `tensors` outputs with row_count rows; row r < row_count is
+ *                 written when some sequence holds it, and rows past cu_rows[seqs] stay as they are
+ * Each value is fl32(code * scale) rounded once to dtype. A position past the table or a page
+ * outside 0 .. pages - 1 leaves its row as it is and is recorded (OPQ_DEVERR_INDEX).
+ * row_count = 0 or seqs = 0 does nothing.
+ */
+opq_status opq_fp8_cache_read(const opq_fp8_cache *cache, const opq_rows *rows, int32_t tensors, int64_t pages,
+                              int64_t page_size, int64_t heads, int32_t dtype, int64_t row_count,
+                              const int32_t *cu_rows, int64_t seqs, const int32_t *page_table, int64_t ld_table,
+                              int64_t table_width, const int32_t *starts, void *stream);
+
+/*
  * opq_device_error — reads and clears the library's device-side error word on
  * the current device (synchronises `stream`). 0 = no error; otherwise a bitmask
  * of OPQ_DEVERR_* recorded by a kernel that returned early, leaving its output
  * invalid: WAIT_TIMEOUT when a bounded wait on a barrier gave up, SMEM_ALIGN when
  * the dynamic shared-memory window did not start on the 1 KiB boundary that the
- * 128-byte-swizzled tensor-core operand stages need.
+ * 128-byte-swizzled tensor-core operand stages need, INDEX when a cache call met a slot or page
+ * number out of range (that entry alone was skipped).
  * After a WAIT_TIMEOUT a caller-provided linear workspace must be zero-filled
  * again before its next use; the arrival counters of opq_linear_noalloc's static
  * array are zeroed by this call itself (a memset on `stream`, synchronised; no
@@ -338,6 +441,7 @@ opq_status opq_linear_noalloc(const uint16_t *x, int64_t M, int64_t K, const uin
  */
 #define OPQ_DEVERR_WAIT_TIMEOUT 1u
 #define OPQ_DEVERR_SMEM_ALIGN 2u
+#define OPQ_DEVERR_INDEX 4u
 opq_status opq_device_error(void *stream, uint32_t *err);
 
 /*
