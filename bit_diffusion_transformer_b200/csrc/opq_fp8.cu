@@ -57,9 +57,11 @@ opq_status launch(Kern kernel, int64_t grid, int threads, size_t smem, int clust
     return e == cudaSuccess ? OPQ_OK : cuda_fail(e);
 }
 
-// dynamic shared memory of a kernel, raised once per device
+// dynamic shared memory of a kernel, raised once per device. `regs`: the registers per thread that a
+// kernel which moves registers between warpgroups (setmaxnreg) was written for; one that was
+// built with any other number is refused, not run.
 template <class Kern>
-opq_status raise_smem(Kern kernel, int bytes, bool (&done)[64]) {
+opq_status raise_smem(Kern kernel, int bytes, bool (&done)[64], int regs = 0) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -69,6 +71,11 @@ opq_status raise_smem(Kern kernel, int bytes, bool (&done)[64]) {
     if (!done[dev]) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return cuda_fail(e);
+        if (regs > 0) {
+            cudaFuncAttributes fa{};
+            if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return cuda_fail(e);
+            if (fa.numRegs != regs) return cuda_fail(cudaErrorInvalidConfiguration);
+        }
         done[dev] = true;
     }
     return OPQ_OK;
@@ -102,15 +109,58 @@ opq_status launch_narrow(const LinearArgs &a, int split, const void *x, int64_t 
                   wmap, xmap, a);
 }
 
+// y [M, N] with row stride ldy, box {32 columns, 32 rows}, 64-byte swizzle (the epilogue's staging)
+opq_status make_y_map(CUtensorMap *map, const LinearArgs &a) {
+    opqhost::EncodeTiledFn fn = opqhost::encode_fn();
+    if (!fn) return OPQ_ERR_CUDA;
+    cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M};
+    cuuint64_t strides[1] = {(cuuint64_t)a.ldy * 2};
+    cuuint32_t box[2] = {32u, 32u};
+    cuuint32_t estr[2] = {1u, 1u};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.y, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? OPQ_OK : cuda_fail((int)r);
+}
+
+template <int CG, int BN, int DT>
+opq_status launch_wide(const LinearArgs &a, const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t K,
+                       void *stream) {
+    using C = WideCfg<CG, BN>;
+    static bool done[64] = {};
+    opq_status s = raise_smem(fp8_wide_kernel<CG, BN, DT>, C::SMEM, done, C::REG_LAUNCH);
+    if (s != OPQ_OK) return s;
+    WideArgs wa{};
+    wa.l = a;
+    wa.tma_store = a.ldy % 8 == 0 ? 1 : 0;
+    CUtensorMap xmap, wmap, ymap;
+    if ((s = make_code_map(&xmap, x, a.M, K, ldx, 128)) != OPQ_OK) return s;
+    if ((s = make_code_map(&wmap, w, a.N, K, ldw, C::W_ROWS)) != OPQ_OK) return s;
+    if (wa.tma_store) {
+        if ((s = make_y_map(&ymap, a)) != OPQ_OK) return s;
+    } else {
+        ymap = xmap;   // not read by the kernel
+    }
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    const int64_t groups = tiles < kSMs / CG ? tiles : kSMs / CG;
+    return launch(fp8_wide_kernel<CG, BN, DT>, groups * CG, C::THREADS, C::SMEM, CG, stream, xmap, wmap, ymap, wa);
+}
+
 struct Fp8Plan {
-    int bx;      // rows of x per tile
-    int split;   // CTAs (a cluster) that share a tile's blocks
+    int cg, bn;  // wide tiles: 128 cg rows of x x bn rows of W (bn 0: narrow tiles)
+    int bx;      // narrow tiles: rows of x
+    int split;   // narrow tiles: CTAs (a cluster) that share a tile's blocks
 };
 
 Fp8Plan make_fp8_plan(int64_t M, int64_t N, int64_t K) {
     Fp8Plan p{};
-    p.bx = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const int64_t kblocks = (K + kBlock - 1) / kBlock;
+    if (M > 128) {
+        p.bn = 256;
+        p.cg = ((M + 127) / 128) * ((N + 255) / 256) > kSMs ? 2 : 1;
+        return p;
+    }
+    p.bx = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const int64_t tiles = ((N + 127) / 128) * ((M + p.bx - 1) / p.bx);
     int64_t s = 2 * kSMs / tiles;
     if (s > 8) s = 8;
@@ -122,6 +172,16 @@ Fp8Plan make_fp8_plan(int64_t M, int64_t N, int64_t K) {
 template <int DT>
 opq_status run_linear(LinearArgs a, const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t K, void *stream) {
     const Fp8Plan p = make_fp8_plan(a.M, a.N, K);
+    if (p.bn) {
+        a.n_tiles = (a.N + p.bn - 1) / p.bn;
+        a.m_tiles = (a.M + 128 * p.cg - 1) / (128 * p.cg);
+        if ((int64_t)a.m_tiles * a.n_tiles > INT32_MAX - 256) return OPQ_ERR_UNSUPPORTED_SHAPE;
+        if (p.bn == 256)
+            return p.cg == 2 ? launch_wide<2, 256, DT>(a, x, ldx, w, ldw, K, stream)
+                             : launch_wide<1, 256, DT>(a, x, ldx, w, ldw, K, stream);
+        return p.cg == 2 ? launch_wide<2, 128, DT>(a, x, ldx, w, ldw, K, stream)
+                         : launch_wide<1, 128, DT>(a, x, ldx, w, ldw, K, stream);
+    }
     a.n_tiles = (a.N + 127) / 128;
     a.m_tiles = (a.M + p.bx - 1) / p.bx;
     switch (p.bx) {

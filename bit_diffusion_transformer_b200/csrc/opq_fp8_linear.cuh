@@ -53,6 +53,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
+// tcgen05.ld: 32 lanes x 32 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+          "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr));
+}
+
 // tanh by the hardware approximation, one MUFU op
 __device__ __forceinline__ float tanh_fast(float x) {
     float y;
@@ -71,10 +84,34 @@ __device__ __forceinline__ float activate(float v, int act) {
     return v;
 }
 
+// mbar_wait with the clock left alone at first: reading the time and the limit costs several
+// hundred cycles, as much as a block's MMAs, and a wait here rarely succeeds at its first try but
+// nearly always within a few. Only a wait that outlasts kSpins tries comes to the time limit.
+constexpr int kSpins = 4096;
+__device__ __forceinline__ bool wait8(uint64_t *bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+    for (int i = 0; i < kSpins; ++i)
+        if (mbar_try_wait(a, parity)) return true;
+    return mbar_wait(bar, parity);
+}
+// one look, without waiting
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // A wait whose verdict is the whole warp's, so that a time-out seen by one lane never leaves the
-// others behind.
+// others behind. Every lane polls: one lane polling for the others, with the branch and the
+// shuffle that takes, measured 40% slower over the whole wide kernel.
 __device__ __forceinline__ bool warp_wait8(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity)) != 0;
+    return __all_sync(0xFFFFFFFFu, wait8(bar, parity)) != 0;
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -99,6 +136,19 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+
+// true in one lane of a converged warp. Around the MMA issue it keeps the loop itself uniform, so
+// that descriptors live in uniform registers; a lane-0 branch around the whole loop moves each
+// operand over from the vector side, 70-90 cycles per MMA against the 64-128 that one runs.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void named_bar(int id, int threads) {
@@ -126,12 +176,16 @@ struct NarrowCfg {
     static constexpr int CHUNK = 512 / BX;
     static constexpr int OFF_SCALE = STAGES * STAGE;
     static constexpr int OFF_BAR = OFF_SCALE + 2 * 512 * 4;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * NACC + 1;
+    static constexpr int NUM_BARS = 2 * STAGES + NACC + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;      // 1 KiB to align the stages
     static constexpr int THREADS = 192;
     static_assert(BX * 128 * 4 <= STAGES * STAGE, "the partial sums reuse the stages");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
+    // one commit per block serves the producer (block i's stage) and the epilogue (block i's sums):
+    // a stage's barrier completes again for block i + STAGES, whose MMAs wait for the epilogue to
+    // have emptied the accumulator of block i + STAGES - NACC, so no completion is missed
+    static_assert(STAGES >= NACC, "done ring");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && 2 * TMEM_COLS <= 512, "two CTAs' TMEM per SM");
 };
 
@@ -145,9 +199,8 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
     uint8_t *smem = smem_raw + pad;
     const uint32_t sbase = smem_u32(smem);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *empty = full + C::STAGES;
-    uint64_t *acc_full = empty + C::STAGES;
-    uint64_t *acc_empty = acc_full + C::NACC;
+    uint64_t *done = full + C::STAGES;         // a stage's MMAs are done: its copies may go, its sums are there
+    uint64_t *acc_empty = done + C::STAGES;
     uint64_t *drain = acc_empty + C::NACC;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,10 +209,9 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
         pdl_launch_dependents();
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&done[s], 1);
         }
         for (int s = 0; s < C::NACC; ++s) {
-            mbar_init(&acc_full[s], 1);
             mbar_init(&acc_empty[s], 4);
         }
         mbar_init(drain, 1);
@@ -188,7 +240,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
             int issued = 0;
             for (int b = b0; b < b1; ++b) {
                 const int s = issued % C::STAGES;
-                if (!(ok = mbar_wait(&empty[s], (uint32_t)(issued / C::STAGES & 1) ^ 1u))) break;
+                if (!(ok = wait8(&done[s], (uint32_t)(issued / C::STAGES & 1) ^ 1u))) break;
                 uint8_t *st = smem + s * C::STAGE;
                 mbar_arrive_expect_tx(&full[s], C::STAGE);
                 tma_load_2d(st, &tmap_w, b * kBlock, n_blk * 128, &full[s]);
@@ -197,26 +249,25 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
             }
             if (!ok)   // a wait gave up: the copies in flight land before the CTA leaves
                 for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
-                    mbar_wait(&full[i % C::STAGES], (uint32_t)(i / C::STAGES & 1));
+                    wait8(&full[i % C::STAGES], (uint32_t)(i / C::STAGES & 1));
         }
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_e4m3_f32(128, BX);
             for (int b = b0, i = 0; b < b1; ++b, ++i) {
                 const int s = i % C::STAGES, a = i % C::NACC;
-                if (!mbar_wait(&acc_empty[a], (uint32_t)(i / C::NACC & 1) ^ 1u)) break;
-                if (!mbar_wait(&full[s], (uint32_t)(i / C::STAGES & 1))) break;
+                if (!wait8(&acc_empty[a], (uint32_t)(i / C::NACC & 1) ^ 1u)) break;
+                if (!wait8(&full[s], (uint32_t)(i / C::STAGES & 1))) break;
                 tc_fence_after();
                 const uint64_t wd = smem_desc_sw128(sbase + s * C::STAGE);
                 const uint64_t xd = smem_desc_sw128(sbase + s * C::STAGE + C::W_BYTES);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)     // 32 columns (32 bytes, 2 descriptor units) each
                     umma_f8_ss(tmem + a * BX, wd + 2 * k, xd + 2 * k, idesc, k > 0);
-                umma_commit(&empty[s]);
-                umma_commit(&acc_full[a]);
+                umma_commit(&done[s]);
             }
             umma_commit(drain);
-            mbar_wait(drain, 0);
+            wait8(drain, 0);
         }
     } else {
         const int q = warp & 3;                      // TMEM lanes 32 q .. 32 q + 31
@@ -251,7 +302,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
                 const int i = b - b0, a = i % C::NACC;
                 // a warp whose wait gave up skips the blocks that are left but still comes to every
                 // chunk's barrier: the other warps may not have seen the time-out
-                if (ok) ok = warp_wait8(&acc_full[a], (uint32_t)(i / C::NACC & 1));
+                if (ok) ok = warp_wait8(&done[i % C::STAGES], (uint32_t)(i / C::STAGES & 1));
                 if (!ok) continue;
                 tc_fence_after();
                 const float *sb = buf + (b - c) * BX;
@@ -314,6 +365,447 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Wide tiles: 128 CG rows of x x BN rows of W, for products bound by the tensor cores. CG = 2
+// joins two SMs in one MMA (cta_group::2): each CTA loads its own 128 rows of x and half of the
+// tile's rows of W, so a tile costs each SM half of the weight traffic; CG = 1 tiles fill the chip
+// when there are few. One persistent CTA (pair) per SM (pair) walks the tiles.
+//   warp 0       TMA producer (both CTAs of a pair; all bytes count on the leader's barrier)
+//   warps 1, 2   TMEM allocation (warp 1); in the leader, the MMA issue, one block each in turn
+//   warp 3       the blocks' scales, by asynchronous copies
+//   warps 4..11  TMEM lane = row of x; warps 4..7 take the tile's left columns, 8..11 the right.
+//                Each block's sums leave TMEM (two accumulators in turn, so the tensor pipe runs
+//                on) and are added times sx[row] sw[block of W]: one scalar per thread and block.
+//                The finished rows go through shared memory and leave by TMA.
+// ---------------------------------------------------------------------------------------------
+template <int CG, int BN>
+struct WideCfg {
+    static constexpr int X_BYTES = 128 * 128;
+    static constexpr int W_ROWS = BN / CG;                 // rows of W in this CTA's shared memory
+    static constexpr int W_BYTES = W_ROWS * 128;
+    static constexpr int STAGE = X_BYTES + W_BYTES;
+    static constexpr int STAGES = CG == 2 ? 163840 / STAGE : 196608 / STAGE;
+    static constexpr int NACC = 2;
+    static constexpr uint32_t TMEM_COLS = NACC * BN;
+    static constexpr int HALF = BN / 2;                    // columns per epilogue warp
+    static constexpr int ROUNDS = HALF / 32;               // 32 columns (64 bytes) staged at a time
+    static constexpr int OUT_BYTES = 32 * 64;              // one warp's rows
+    // pairs run many tiles each: their stores overlap the next tile's MMAs, from three buffers
+    static constexpr int OUT_BUFS = CG == 2 ? 3 : 1;
+    // Scales of the blocks under way: 128 rows' and two of W per slot. Block i's copies start when
+    // the MMAs of block i - STAGES are done, which says that the epilogue is past block
+    // i - STAGES - NACC, so STAGES + NACC slots are enough.
+    static constexpr int RING = STAGES + 2 <= 8 ? 8 : 16;
+    static constexpr int LAG = STAGES >= 6 ? 2 : 1;        // blocks whose scales may still be in flight
+    static constexpr int SCALE_WORDS = 128 + 2;
+    static constexpr int OFF_OUT = STAGES * STAGE;
+    static constexpr int OFF_SCALE = OFF_OUT + 8 * OUT_BUFS * OUT_BYTES;
+    static constexpr int OFF_BIAS = OFF_SCALE + RING * SCALE_WORDS * 4;   // 8 warps x HALF 16-bit values
+    static constexpr int OFF_BAR = OFF_BIAS + 8 * HALF * 2;
+    static constexpr int NUM_BARS = 2 * STAGES + NACC + 1;
+    static constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM = OFF_TMEM + 16;             // the kernel checks the 1 KiB alignment
+    static constexpr int THREADS = 384;
+    // The epilogue's two warpgroups hold a row's sums (HALF) and 64 columns in flight; the first
+    // warpgroup gives up what they take. The launch checks that the kernel was built for REG_LAUNCH.
+    static constexpr int REG_LAUNCH = 168, REG_EPI = 224, REG_PROD = 3 * REG_LAUNCH - 2 * REG_EPI;
+    static_assert(THREADS * REG_LAUNCH <= 65536 && REG_PROD % 8 == 0 && REG_PROD >= 40, "register split");
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(STAGES >= NACC && RING >= STAGES + NACC && LAG < STAGES, "done ring (as for the narrow tiles)");
+    static_assert(STAGE % 1024 == 0 && HALF % 64 == 0 && TMEM_COLS <= 512, "layout");
+};
+
+struct WideArgs {
+    LinearArgs l;
+    int tma_store;      // y rows are 16-byte aligned
+};
+
+template <int CG>
+__device__ __forceinline__ void umma_f8_cg(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    if (CG == 1) {
+        umma_f8_ss(d_tmem, a_desc, b_desc, idesc, accumulate);
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    }
+}
+// arrive on `bar` (in every CTA of the pair) when the MMAs issued so far are done
+template <int CG>
+__device__ __forceinline__ void umma_commit_cg(uint64_t *bar) {
+    if (CG == 1) {
+        umma_commit(bar);
+    } else {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+    }
+}
+// the same, in this CTA only
+template <int CG>
+__device__ __forceinline__ void umma_commit_own(uint64_t *bar) {
+    if (CG == 1)
+        umma_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     ::"r"(smem_u32(bar)) : "memory");
+}
+// a tile copy into this CTA, counted on the barrier at `bar` (the leader's, for a pair)
+template <int CG>
+__device__ __forceinline__ void tma_load_cg(uint32_t dst, const void *tmap, int32_t c0, int32_t c1, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(tmap), "r"(c0), "r"(c1), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(tmap), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_alloc_cg(uint32_t *slot, uint32_t cols) {
+    if (CG == 1) {
+        tmem_alloc(slot, cols);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc_cg(uint32_t addr, uint32_t cols) {
+    if (CG == 1)
+        tmem_dealloc(addr, cols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// One arrival on a barrier of any CTA of the cluster, by the lanes with `on` (a predicate, no branch).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr, bool on) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}"
+        ::"r"(addr), "r"((int)on) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// byte offset of 16-byte chunk `chunk` (0..3) of row `row` in a 64-byte-swizzled tile
+__device__ __forceinline__ uint32_t sw64_offset(uint32_t row, uint32_t chunk) {
+    return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
+// a thread's bulk stores: groups, and waits for all but N of them (to be read; to be done)
+__device__ __forceinline__ void tma_store_2d(const void *tmap, uint32_t src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(tmap), "r"(c0), "r"(c1), "r"(src) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+template <int CG, int BN, int DT>
+__global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                    const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ WideArgs W) {
+    using C = WideCfg<CG, BN>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const LinearArgs &A = W.l;
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *done = full + C::STAGES;         // a stage's MMAs are done: its copies may go, its sums are there
+    uint64_t *acc_empty = done + C::STAGES;
+    uint64_t *drain = acc_empty + C::NACC;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    // the swizzled stages need 1 KiB boundaries; the same for every CTA of the launch
+    if ((sbase & 1023u) != 0) {
+        if (threadIdx.x == 0) atomicOr(&g_error, kErrSmemAlign);
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        pdl_launch_dependents();
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1 + CG);   // the leader's producer and each CTA's scale warp
+            mbar_init(&done[s], 1);
+        }
+        for (int s = 0; s < C::NACC; ++s) {
+            mbar_init(&acc_empty[s], 8 * CG);
+        }
+        mbar_init(drain, 2);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmap_x);
+        tma_prefetch_desc(&tmap_w);
+        if (W.tma_store) tma_prefetch_desc(&tmap_y);
+    }
+    if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, C::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) {
+        cluster_arrive();   // the peer's barriers are ready before anything arrives on them
+        cluster_wait();
+    }
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int tiles = A.m_tiles * A.n_tiles;
+    const int first = (int)blockIdx.x / CG, step = (int)gridDim.x / CG;
+
+    if (warp < 4) {
+        setmaxnreg_dec<C::REG_PROD>();
+        if (warp == 0 && lane == 0) {
+            pdl_wait();
+            bool ok = true;
+            int64_t issued = 0;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int t = first; t < tiles && ok; t += step) {
+                const int n_blk = t / A.m_tiles, m_blk = t - n_blk * A.m_tiles;
+                const int m0 = m_blk * 128 * CG + (int)rank * 128, n0 = n_blk * BN + (int)rank * C::W_ROWS;
+                for (int b = 0; b < A.kblocks; ++b) {
+                    if (!(ok = wait8(&done[s], ph ^ 1u))) break;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::STAGE);
+                    const uint32_t st = sbase + s * C::STAGE;
+                    const uint32_t bar = CG == 2 ? mapa(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+                    tma_load_cg<CG>(st, &tmap_x, b * kBlock, m0, bar);
+                    tma_load_cg<CG>(st + C::X_BYTES, &tmap_w, b * kBlock, n0, bar);
+                    ++issued;
+                    if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+            const int64_t tail0 = issued > C::STAGES ? issued - C::STAGES : 0;
+            for (int64_t i = tail0; i < issued; ++i) {
+                const int ts = (int)(i % C::STAGES);
+                const uint32_t tp = (uint32_t)(i / C::STAGES & 1);
+                if (ok)
+                    ok = wait8(&done[ts], tp);    // no commit arrives after this CTA has left
+                else if (rank == 0)
+                    wait8(&full[ts], tp);          // a wait gave up: the copies in flight land first
+            }
+        }
+        if ((warp == 1 || warp == 2) && rank == 0) {
+            // Two warps issue in turn, one per accumulator: a block's two waits, four MMAs and commit
+            // take one warp longer than the MMAs run.
+            constexpr uint32_t idesc = idesc_e4m3_f32(128 * CG, BN);
+            const uint64_t xd0 = smem_desc_sw128(sbase), wd0 = smem_desc_sw128(sbase + C::X_BYTES);
+            const int a = warp - 1;
+            const uint32_t d = tmem + (uint32_t)a * BN;
+            const int64_t blocks = first < tiles ? (int64_t)((tiles - 1 - first) / step + 1) * A.kblocks : 0;
+            int s = a;
+            uint32_t ph = 0, aph = 0;
+            for (int64_t i = a; i < blocks; i += 2) {
+                // the operands first: they are there long before the accumulator comes back
+                if (!warp_wait8(&full[s], ph)) break;
+                if (!warp_wait8(&acc_empty[a], aph ^ 1u)) break;
+                tc_fence_after();
+                const uint64_t xd = xd0 + (uint32_t)(s * (C::STAGE >> 4)), wd = wd0 + (uint32_t)(s * (C::STAGE >> 4));
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma_f8_cg<CG>(d, xd + 2 * k, wd + 2 * k, idesc, k > 0);
+                    umma_commit_cg<CG>(&done[s]);
+                }
+                __syncwarp();
+                s += 2;
+                if (s >= C::STAGES) { s -= C::STAGES; ph ^= 1u; }
+                aph ^= 1u;
+            }
+            if (elect_one()) umma_commit_own<CG>(drain);
+            __syncwarp();
+            warp_wait8(drain, 0);
+        }
+        if (warp == 3) {
+            // Scales: asynchronous copies into the ring; a block's arrival counts on the barrier that
+            // its MMAs wait for, so that whoever sees its sums sees its scales too.
+            pdl_wait();
+            const uint32_t ring = smem_u32(smem + C::OFF_SCALE);
+            const uint32_t bar0 = CG == 2 ? mapa(smem_u32(full), 0) : smem_u32(full);   // the leader's
+            bool ok = true;
+            int s = 0, sl = 0, behind = 0;
+            uint32_t ph = 0, slot = 0;
+            auto announce = [&]() {
+                __syncwarp();
+                mbar_arrive_cluster(bar0 + sl * 8, lane == 0);
+                if (++sl == C::STAGES) sl = 0;
+            };
+            for (int t = first; t < tiles && ok; t += step) {
+                const int n_blk = t / A.m_tiles, m_blk = t - n_blk * A.m_tiles;
+                const int m = m_blk * 128 * CG + (int)rank * 128 + lane;
+                const float *gx = A.xs;
+                const float *gw = A.ws;
+                const int nh = n_blk * BN + (lane & 1) * C::HALF;
+                if (nh < A.N) gw += nh / kBlock;
+                for (int b = 0; b < A.kblocks; ++b) {
+                    if (!(ok = warp_wait8(&done[s], ph ^ 1u))) break;
+                    const uint32_t dst = ring + slot;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) cp_async4(dst + (u * 32 + lane) * 4, gx + (m + u * 32 < A.M ? m + u * 32 : 0));
+                    if (lane < 2) cp_async4(dst + (128 + lane) * 4, gw);
+                    cp_async_commit();
+                    gx += A.ld_xs;
+                    gw += A.ld_ws;
+                    cp_async_wait<C::LAG>();
+                    if (behind == C::LAG) announce(); else ++behind;
+                    slot = slot == (C::RING - 1) * C::SCALE_WORDS * 4 ? 0 : slot + C::SCALE_WORDS * 4;
+                    if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+            cp_async_wait<0>();
+            if (ok)
+                for (; behind > 0; --behind) announce();
+        }
+    } else {
+        setmaxnreg_inc<C::REG_EPI>();
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + half * C::HALF;
+        uint8_t *stage = smem + C::OFF_OUT + (warp - 4) * C::OUT_BUFS * C::OUT_BYTES;
+        uint16_t *bias_s = reinterpret_cast<uint16_t *>(smem + C::OFF_BIAS) + (warp - 4) * C::HALF;
+        bool ok = true;
+        int a = 0, sd = 0;
+        uint32_t sph = 0;
+        const uint32_t acc_bar = CG == 2 ? mapa(smem_u32(acc_empty), 0) : smem_u32(acc_empty);   // the leader's
+        const uint32_t my_scale = smem_u32(smem + C::OFF_SCALE) + (q * 32 + lane) * 4;
+        const uint32_t w_scale = smem_u32(smem + C::OFF_SCALE) + (128 + half) * 4;
+        uint32_t slot = 0;
+        int ob = 0;
+        bool ready = false;      // the next block's sums are known to be complete, and `s` is its scale
+        float s = 0.0f;
+        pdl_wait();
+        for (int t = first; t < tiles && ok; t += step) {
+            const int n_blk = t / A.m_tiles, m_blk = t - n_blk * A.m_tiles;
+            const int mw = m_blk * 128 * CG + (int)rank * 128 + q * 32;     // the warp's first row
+            const int n0 = n_blk * BN + half * C::HALF;                     // and column
+            if (A.bias != nullptr) {
+                __syncwarp();
+                for (int j = lane; j < C::HALF; j += 32) bias_s[j] = n0 + j < A.N ? __ldg(A.bias + n0 + j) : (uint16_t)0;
+            }
+            float2 acc[C::HALF / 2];
+#pragma unroll
+            for (int j = 0; j < C::HALF / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int b = 0; b < A.kblocks; ++b) {
+                if (!ready) {
+                    if (!(ok = warp_wait8(&done[sd], sph))) break;
+                    s = lds_f32(my_scale + slot) * lds_f32(w_scale + slot);
+                }
+                tc_fence_after();
+                if (++sd == C::STAGES) { sd = 0; sph ^= 1u; }
+                slot = slot == (C::RING - 1) * C::SCALE_WORDS * 4 ? 0 : slot + C::SCALE_WORDS * 4;
+                const float2 s2 = make_float2(s, s);
+                const uint32_t ta = lane_base + a * BN;
+                // 64 columns at a time; the next 32 are asked for as soon as their registers are free, and
+                // the accumulator is handed back before the last sums are added
+                float r[64];
+                tmem_ld32(ta, r);
+                tmem_ld32(ta + 32, r + 32);
+                // is the next block there already? Asked now, answered for free when this one is added
+                const bool peek = mbar_test_wait(&done[sd], sph);
+                tmem_ld_wait();
+                auto add32 = [&](int c0, const float *v) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[c0 / 2 + j] = fma2(make_float2(v[2 * j], v[2 * j + 1]), s2, acc[c0 / 2 + j]);
+                };
+                if (C::HALF == 128) {
+                    add32(0, r);
+                    tmem_ld32(ta + 64, r);
+                    add32(32, r + 32);
+                    tmem_ld32(ta + 96, r + 32);
+                    tmem_ld_wait();
+                }
+                // (the wait above is the whole warp's: one lane may speak for it)
+                tc_fence_before();
+                mbar_arrive_cluster(acc_bar + a * 8, lane == 0);
+                ready = __all_sync(0xFFFFFFFFu, peek) != 0;
+                if (ready) s = lds_f32(my_scale + slot) * lds_f32(w_scale + slot);
+                add32(C::HALF - 64, r);
+                add32(C::HALF - 32, r + 32);
+                if (++a == C::NACC) a = 0;
+            }
+            if (!ok) break;
+            // The rows' outputs, 32 columns at a time: each lane leaves its row's 64 bytes in shared
+            // memory in the TMA store's swizzle. The store is asynchronous because all CTAs finish
+            // their tiles together: 10 MB at once, 2 us of L2 writes (stored by the warps
+            // themselves that was 4300 cycles a tile).
+#pragma unroll
+            for (int rd = 0; rd < C::ROUNDS; ++rd) {
+                uint8_t *buf = stage + ob * C::OUT_BYTES;
+                uint32_t o[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float2 v = acc[rd * 16 + j];
+                    if (A.bias != nullptr) {
+                        const float2 bv = unpack16<DT>(*reinterpret_cast<const uint32_t *>(bias_s + rd * 32 + 2 * j));
+                        v.x += bv.x;
+                        v.y += bv.y;
+                    }
+                    if (A.act != ACT_NONE) {
+                        v.x = activate(v.x, A.act);
+                        v.y = activate(v.y, A.act);
+                    }
+                    o[j] = pack16<DT>(v);
+                }
+                bulk_wait_read<C::OUT_BUFS - 1>();     // the store that last used this buffer has read it
+                __syncwarp();
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    *reinterpret_cast<uint4 *>(buf + sw64_offset((uint32_t)lane, (uint32_t)ch)) =
+                        make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
+                const int nr = n0 + rd * 32;
+                if (W.tma_store) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (nr < A.N && mw < A.M) tma_store_2d(&tmap_y, smem_u32(buf), nr, mw);
+                        bulk_commit();
+                    }
+                } else {
+                    // rows that TMA cannot address: lanes along the columns
+                    __syncwarp();
+                    const int rows = A.M - mw < 32 ? A.M - mw : 32;
+                    if (nr + lane < A.N) {
+                        uint16_t *yr = A.y + (int64_t)mw * A.ldy + nr + lane;
+#pragma unroll 4
+                        for (int r = 0; r < rows; ++r, yr += A.ldy)
+                            *yr = *reinterpret_cast<const uint16_t *>(
+                                buf + sw64_offset((uint32_t)r, (uint32_t)(lane >> 3)) + (lane & 7) * 2);
+                    }
+                }
+                if (++ob == C::OUT_BUFS) ob = 0;
+            }
+        }
+        bulk_wait_all();
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) {
+        cluster_arrive();   // the pair leaves together: neither's barriers or TMEM are in use
+        cluster_wait();
+    }
+    if (warp == 1) tmem_dealloc_cg<CG>(tmem, C::TMEM_COLS);
 }
 
 }  // namespace opqfp8
