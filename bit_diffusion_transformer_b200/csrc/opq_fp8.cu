@@ -245,19 +245,20 @@ opq_status check_cache(const opq_fp8_cache *cache, const opq_rows *rows, int32_t
     return OPQ_OK;
 }
 
-template <int DT>
-opq_status run_write(const WriteArgs &a, int lanes, void *stream) {
-    // one item per lane group for short calls (latency: the work spreads over more SMs), four for
-    // long ones (four loads in flight per thread)
-    const int64_t groups = kWriteThreads / lanes;
-    const bool longer = (int64_t)a.items > groups * 4 * kSMs;
-    const int64_t per = groups * (longer ? 4 : 1);
-    const int64_t grid = ((int64_t)a.items + per - 1) / per;
-    if (lanes == 8)
-        return longer ? launch(fp8_cache_write_kernel<DT, 8, 4>, grid, kWriteThreads, 0, 1, stream, a)
-                      : launch(fp8_cache_write_kernel<DT, 8, 1>, grid, kWriteThreads, 0, 1, stream, a);
-    return longer ? launch(fp8_cache_write_kernel<DT, 16, 4>, grid, kWriteThreads, 0, 1, stream, a)
-                  : launch(fp8_cache_write_kernel<DT, 16, 1>, grid, kWriteThreads, 0, 1, stream, a);
+template <int DT, int LANES>
+opq_status run_write(WriteArgs a, void *stream) {
+    // the CTA's lane groups take `pass` columns of as many tokens as fit at a time; short calls
+    // take one such round per CTA (latency: the work spreads over more SMs), long ones four
+    // (four loads in flight per thread)
+    const int groups = kWriteThreads / LANES;
+    a.pass = a.cols < groups ? a.cols : groups;
+    a.pass_div = FastDiv::make((uint32_t)a.pass);
+    const int step = groups / a.pass;
+    const bool longer = a.tokens > (int64_t)step * 2 * kSMs;
+    a.token_block = longer ? (step * 4 < kWriteTokens ? step * 4 : kWriteTokens) : (step < kWriteTokens ? step : kWriteTokens);
+    const int64_t grid = (a.tokens + a.token_block - 1) / a.token_block;
+    return longer ? launch(fp8_cache_write_kernel<DT, LANES, 4>, grid, kWriteThreads, 0, 1, stream, a)
+                  : launch(fp8_cache_write_kernel<DT, LANES, 1>, grid, kWriteThreads, 0, 1, stream, a);
 }
 
 }  // namespace
@@ -341,25 +342,26 @@ opq_status opq_fp8_cache_write(const opq_fp8_cache *cache, const opq_rows *rows,
     if (s == OPQ_OK) s = check_device({slots});
     if (s != OPQ_OK) return s;
     WriteArgs a{};
-    int64_t per[2] = {0, 0};
-    int lanes = 8;
+    int64_t cols[2] = {0, 0};
+    bool narrow = true;   // eight lanes hold a whole block of up to 64 channels
     for (int i = 0; i < tensors; ++i) {
         a.side[i] = make_side(cache[i], rows[i]);
-        per[i] = heads * a.side[i].blocks;
+        cols[i] = heads * a.side[i].blocks;
         a.blocks[i] = FastDiv::make((uint32_t)a.side[i].blocks);
-        if (a.side[i].dim > 64) lanes = 16;   // eight lanes hold a whole block of up to 64 channels
+        if (a.side[i].dim > 64) narrow = false;
     }
     if (tensors == 1) a.blocks[1] = a.blocks[0];
-    if (per[0] + per[1] > INT32_MAX || tokens > INT32_MAX / (per[0] + per[1]) - 64) return OPQ_ERR_UNSUPPORTED_SHAPE;
+    if (cols[0] + cols[1] > INT32_MAX - 4096 || tokens > INT32_MAX) return OPQ_ERR_UNSUPPORTED_SHAPE;
     a.slots = slots;
     a.slot_count = pages * page_size;
     a.page_size = page_size;
     a.tokens = tokens;
-    a.first_v = (uint32_t)per[0];
-    a.per_token = FastDiv::make((uint32_t)(per[0] + per[1]));
+    a.cols0 = (int)cols[0];
+    a.cols = (int)(cols[0] + cols[1]);
     a.page_div = FastDiv::make((uint32_t)page_size);
-    a.items = (uint32_t)(tokens * (per[0] + per[1]));
-    return dtype == OPQ_DTYPE_BF16 ? run_write<DT_BF16>(a, lanes, stream) : run_write<DT_FP16>(a, lanes, stream);
+    if (dtype == OPQ_DTYPE_BF16)
+        return narrow ? run_write<DT_BF16, 8>(a, stream) : run_write<DT_BF16, 16>(a, stream);
+    return narrow ? run_write<DT_FP16, 8>(a, stream) : run_write<DT_FP16, 16>(a, stream);
 }
 
 opq_status opq_fp8_cache_read(const opq_fp8_cache *cache, const opq_rows *rows, int32_t tensors, int64_t pages,
@@ -376,15 +378,18 @@ opq_status opq_fp8_cache_read(const opq_fp8_cache *cache, const opq_rows *rows, 
     if (s == OPQ_OK && starts) s = check_device({starts});
     if (s != OPQ_OK) return s;
     ReadArgs a{};
+    int64_t cols[2] = {0, 0};
     for (int i = 0; i < tensors; ++i) {
         a.side[i] = make_side(cache[i], rows[i]);
-        a.chunks[i] = (uint32_t)(heads * (cache[i].head_dim / 16));
-        a.head_chunks[i] = FastDiv::make((uint32_t)(cache[i].head_dim / 16));
+        cols[i] = heads * (cache[i].head_dim / 8);
+        a.head_chunks[i] = FastDiv::make((uint32_t)(cache[i].head_dim / 8));
     }
     if (tensors == 1) a.head_chunks[1] = a.head_chunks[0];
-    const int64_t per_row = (int64_t)a.chunks[0] + a.chunks[1];
-    if (per_row > INT32_MAX / 64) return OPQ_ERR_UNSUPPORTED_SHAPE;
-    a.per_row = FastDiv::make((uint32_t)per_row);
+    if (cols[0] + cols[1] > INT32_MAX / 64) return OPQ_ERR_UNSUPPORTED_SHAPE;
+    a.cols0 = (int)cols[0];
+    a.cols = (int)(cols[0] + cols[1]);
+    a.pass = a.cols < kReadThreads ? a.cols : kReadThreads;
+    a.pass_div = FastDiv::make((uint32_t)a.pass);
     a.page_div = FastDiv::make((uint32_t)page_size);
     a.cu_rows = cu_rows;
     a.page_table = page_table;
@@ -395,14 +400,13 @@ opq_status opq_fp8_cache_read(const opq_fp8_cache *cache, const opq_rows *rows, 
     a.page_size = page_size;
     a.rows = row_count;
     a.seqs = (int)seqs;
-    a.tensors = tensors;
-    // about 2048 chunks per CTA (eight per thread), fewer rows when there are few
-    int64_t rb = 2048 / per_row;
-    if (rb > (row_count + kSMs - 1) / kSMs) rb = (row_count + kSMs - 1) / kSMs;
+    // a CTA that finds its rows' slots waits for memory twice before its first load: enough rows per
+    // CTA that all of them run at once, fewer when there are few rows (latency)
+    const int64_t rb = (row_count + 4 * kSMs - 1) / (4 * kSMs);
     a.row_block = (int)(rb < 1 ? 1 : rb > kReadRows ? kReadRows : rb);
     const int64_t grid = (row_count + a.row_block - 1) / a.row_block;
-    return dtype == OPQ_DTYPE_BF16 ? launch(fp8_cache_read_kernel<DT_BF16, 4>, grid, kReadThreads, 0, 1, stream, a)
-                                   : launch(fp8_cache_read_kernel<DT_FP16, 4>, grid, kReadThreads, 0, 1, stream, a);
+    return dtype == OPQ_DTYPE_BF16 ? launch(fp8_cache_read_kernel<DT_BF16, 8>, grid, kReadThreads, 0, 1, stream, a)
+                                   : launch(fp8_cache_read_kernel<DT_FP16, 8>, grid, kReadThreads, 0, 1, stream, a);
 }
 
 }  // extern "C"

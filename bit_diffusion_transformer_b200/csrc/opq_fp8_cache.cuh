@@ -36,70 +36,101 @@ struct WriteArgs {
     int64_t slot_count;      // pages * page_size
     int64_t page_size;
     int64_t tokens;
-    uint32_t items;          // tokens x per_token
-    uint32_t first_v;        // items of side 0 per token
-    FastDiv per_token, blocks[2], page_div;
+    int token_block;         // tokens per CTA
+    int cols, cols0;         // (head, block) columns of both sides, of side 0
+    int pass;                // columns that the CTA's lane groups take at a time
+    FastDiv blocks[2], page_div, pass_div;
 };
 
 constexpr int kWriteThreads = 256;
+constexpr int kWriteTokens = 64;     // most tokens per CTA
 
-// LANES lanes (eight channels each) per (token, head, block) item; U items per lane group, all
-// loads ahead of the first maximum.
+// The offsets of a token's slot in one side's codes and scales.
+struct SlotAt {
+    int64_t codes, scales;
+};
+__device__ __forceinline__ SlotAt slot_at(const CacheSide &S, int64_t page, int64_t off) {
+    return {page * S.page_stride + off * S.token_stride, page * S.scale_page_stride + off * S.scale_token_stride};
+}
+
+// A CTA takes token_block tokens. One thread per token looks its slot up; then each group of LANES
+// lanes (eight channels a lane) keeps one (head, block) column and walks the tokens, U at a time with
+// their loads ahead of the first maximum: what depends on the column is worked out once.
 template <int DT, int LANES, int U>
 __global__ void __launch_bounds__(kWriteThreads) fp8_cache_write_kernel(const __grid_constant__ WriteArgs A) {
-    constexpr int GROUPS = kWriteThreads / LANES;
+    __shared__ SlotAt s_at[2][kWriteTokens];    // codes -1: a token that is not written
     opqdev::pdl_launch_dependents();
     const int g = threadIdx.x / LANES, l = threadIdx.x % LANES;
+    const int64_t t0 = (int64_t)blockIdx.x * A.token_block;
+    const int n = (int)(A.tokens - t0 < A.token_block ? A.tokens - t0 : A.token_block);
     opqdev::pdl_wait();
-    uint4 v[U];
-    uint8_t *dst[U];
-    float *sdst[U];
+    auto find_slot = [&](int i) {
+        const int64_t slot = A.slots[t0 + i];
+        SlotAt k{-1, 0}, w{-1, 0};
+        if (slot >= A.slot_count) {
+            atomicOr(&opqdev::g_error, kErrIndex);
+        } else if (slot >= 0) {
+            const int64_t page = page_of(slot, A.page_div, A.page_size), off = slot - page * A.page_size;
+            k = slot_at(A.side[0], page, off);
+            w = slot_at(A.side[1], page, off);
+        }
+        s_at[0][i] = k;
+        s_at[1][i] = w;
+    };
+    const int row = (int)A.pass_div.div((uint32_t)g), lane_col = g - row * A.pass, step = (int)A.pass_div.div(kWriteThreads / LANES);
+    for (int strip = 0; strip < A.cols; strip += A.pass) {
+        const int col = strip + lane_col;
+        const bool on = row < step && col < A.cols;
+        const int which = col >= A.cols0 ? 1 : 0;
+        const CacheSide &S = A.side[which];
+        const uint32_t rest = on ? (uint32_t)(col - (which ? A.cols0 : 0)) : 0u;
+        const uint32_t head = A.blocks[which].div(rest), blk = rest - head * A.blocks[which].d;
+        const int c = (int)blk * kBlock + l * 8;
+        const bool live = on && c < S.dim;
+        const uint8_t *src = S.rows + 2 * ((int64_t)head * S.row_head_stride + c + t0 * S.row_stride);
+        uint8_t *codes = S.codes + (int64_t)head * S.head_stride + c;
+        float *scales = S.scales + (int64_t)head * S.scale_head_stride + blk;
+        // every lane walks the same number of rounds: the maxima are shuffled over the whole warp.
+        // The rows are there whatever their slots say, so the first round's loads leave before the
+        // slots are known.
+        uint4 v[U];
+        auto load = [&](int i0) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const uint32_t item = (uint32_t)blockIdx.x * (GROUPS * U) + i * GROUPS + g;
-        v[i] = make_uint4(0, 0, 0, 0);
-        dst[i] = nullptr;
-        sdst[i] = nullptr;
-        if (item < A.items) {
-            const uint32_t t = A.per_token.div(item);
-            uint32_t rest = item - t * A.per_token.d;
-            const int which = rest >= A.first_v ? 1 : 0;
-            rest -= which ? A.first_v : 0u;
-            const CacheSide &S = A.side[which];
-            const uint32_t head = A.blocks[which].div(rest);
-            const uint32_t blk = rest - head * A.blocks[which].d;
-            const int c = (int)blk * kBlock + l * 8;
-            const int64_t slot = A.slots[t];
-            if (slot >= A.slot_count) {
-                if (l == 0) atomicOr(&opqdev::g_error, kErrIndex);
-            } else if (slot >= 0) {
-                const int64_t page = page_of(slot, A.page_div, A.page_size), off = slot - page * A.page_size;
-                if (c < S.dim) {
-                    v[i] = *reinterpret_cast<const uint4 *>(
-                        S.rows + 2 * ((int64_t)t * S.row_stride + (int64_t)head * S.row_head_stride + c));
-                    dst[i] = S.codes + page * S.page_stride + off * S.token_stride + (int64_t)head * S.head_stride + c;
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * step + row;
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (live && i < n) v[u] = *reinterpret_cast<const uint4 *>(src + 2 * i * S.row_stride);
+            }
+        };
+        load(0);
+        if (strip == 0) {
+            if (threadIdx.x < (unsigned)n) find_slot(threadIdx.x);
+            __syncthreads();
+        }
+        for (int i0 = 0; i0 < n; i0 += step * U) {
+            uint32_t mx[U];
+            block_maxima<DT, LANES, U>(v, mx);
+            uint32_t own = mx[0];
+#pragma unroll
+            for (int u = 1; u < U; ++u) own = l % U == u ? mx[u] : own;
+            const float om = floored(bits_to_float<DT>(own)), omul = block_mul(om);
+            if (on && l < U) {
+                const int i = i0 + l * step + row;
+                if (i < n && s_at[which][i].codes >= 0) scales[s_at[which][i].scales] = block_scale(om);
+            }
+            uint2 o[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) o[u] = encode8<DT>(v[u], __shfl_sync(0xFFFFFFFFu, omul, u, U));
+            load(i0 + step * U);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * step + row;
+                if (live && i < n) {
+                    const int64_t at = s_at[which][i].codes;
+                    if (at >= 0) *reinterpret_cast<uint2 *>(codes + at) = o[u];
                 }
-                if (l == 0)
-                    sdst[i] = S.scales + page * S.scale_page_stride + off * S.scale_token_stride +
-                              (int64_t)head * S.scale_head_stride + blk;
             }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        uint32_t mx = absmax8(v[i]);
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        const bool wild = mx >= kInfBits<DT>;
-        if (__any_sync(0xFFFFFFFFu, wild)) {
-            mx = absmax8_finite<DT>(v[i]);
-#pragma unroll
-            for (int o = LANES / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        }
-        const BlockScale s(bits_to_float<DT>(mx));
-        const uint2 c = encode8<DT>(v[i], s, wild);
-        if (dst[i]) *reinterpret_cast<uint2 *>(dst[i]) = c;
-        if (sdst[i]) *sdst[i] = s.scale;
     }
 }
 
@@ -113,95 +144,100 @@ struct ReadArgs {
     int64_t pages, page_size;
     int64_t rows;
     int seqs;
-    int tensors;
     int row_block;               // rows per CTA
-    uint32_t chunks[2];          // 16-code chunks per row of a side: heads x dim / 16
-    FastDiv head_chunks[2];      // dim / 16
-    FastDiv per_row;             // chunks of both sides
-    FastDiv page_div;            // page_size
+    int cols, cols0;             // 8-code chunks per row of both sides, of side 0 (heads x dim / 8)
+    int pass;                    // chunks that the CTA's threads take at a time
+    FastDiv head_chunks[2];      // dim / 8
+    FastDiv page_div, pass_div;
 };
 
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 16;    // most rows per CTA
+constexpr int kReadRows = 64;    // most rows per CTA
+constexpr int kReadSeqs = 511;   // most sequences whose cu_rows are staged
 
 // A CTA takes row_block consecutive output rows: one thread per row finds the sequence (binary
-// search in cu_rows), the page and the slot; then every lane decodes 16-code chunks (16 bytes
-// in, 32 out).
+// search in cu_rows, staged in shared memory for up to kReadSeqs sequences: one trip to memory
+// instead of one per step), the page and the slot; then every thread keeps one 8-code chunk of the
+// row (8 bytes in, 16 out: a warp's stores are contiguous) and walks the rows, U loads ahead: what depends on the chunk is worked out
+// once.
 template <int DT, int U>
 __global__ void __launch_bounds__(kReadThreads) fp8_cache_read_kernel(const __grid_constant__ ReadArgs A) {
-    __shared__ int64_t s_page[kReadRows];   // -1: a row that is not read
-    __shared__ int32_t s_off[kReadRows];
+    __shared__ SlotAt s_at[2][kReadRows];    // codes -1: a row that is not read
+    __shared__ int32_t s_cu[kReadSeqs + 1];
     opqdev::pdl_launch_dependents();
     const int64_t r0 = (int64_t)blockIdx.x * A.row_block;
+    const int n = (int)(A.rows - r0 < A.row_block ? A.rows - r0 : A.row_block);
     opqdev::pdl_wait();
-    if (threadIdx.x < (unsigned)A.row_block) {
+    const int32_t *cu = A.cu_rows;
+    if (A.seqs <= kReadSeqs) {
+        for (int i = threadIdx.x; i <= A.seqs; i += kReadThreads) s_cu[i] = A.cu_rows[i];
+        __syncthreads();
+        cu = s_cu;
+    }
+    if (threadIdx.x < (unsigned)n) {
         const int64_t r = r0 + threadIdx.x;
-        int64_t page = -1, off = 0;
-        if (r < A.rows && r >= A.cu_rows[0] && r < A.cu_rows[A.seqs]) {
-            int lo = 0, hi = A.seqs;            // cu_rows[lo] <= r < cu_rows[hi]
+        SlotAt k{-1, 0}, w{-1, 0};
+        if (r >= cu[0] && r < cu[A.seqs]) {
+            int lo = 0, hi = A.seqs;            // cu[lo] <= r < cu[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (A.cu_rows[mid] <= r) lo = mid; else hi = mid;
+                if (cu[mid] <= r) lo = mid; else hi = mid;
             }
-            const int64_t pos = r - A.cu_rows[lo] + (A.starts ? (int64_t)A.starts[lo] : 0);
-            const int64_t pi = pos >= 0 ? page_of(pos, A.page_div, A.page_size) : 0;
-            bool ok = pos >= 0 && pi < A.table_width;
-            if (ok) {
-                page = A.page_table[(int64_t)lo * A.ld_table + pi];
-                off = pos - pi * A.page_size;
-                ok = page >= 0 && page < A.pages;
-            }
-            if (!ok) {
-                page = -1;
+            const int64_t pos = r - cu[lo] + (A.starts ? (int64_t)A.starts[lo] : 0);
+            const int64_t pi = pos >= 0 ? page_of(pos, A.page_div, A.page_size) : A.table_width;
+            const int64_t page = pi < A.table_width ? (int64_t)A.page_table[(int64_t)lo * A.ld_table + pi] : -1;
+            if (page >= 0 && page < A.pages) {
+                k = slot_at(A.side[0], page, pos - pi * A.page_size);
+                w = slot_at(A.side[1], page, pos - pi * A.page_size);
+            } else {
                 atomicOr(&opqdev::g_error, kErrIndex);
             }
         }
-        s_page[threadIdx.x] = page;
-        s_off[threadIdx.x] = (int32_t)off;
+        s_at[0][threadIdx.x] = k;
+        s_at[1][threadIdx.x] = w;
     }
     __syncthreads();
-    const uint32_t n = (uint32_t)A.row_block * A.per_row.d;
-    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kReadThreads * U) {
-        uint4 v[U];
-        float sc[U];
-        uint8_t *dst[U];
+    const int row = (int)A.pass_div.div(threadIdx.x), lane_col = (int)threadIdx.x - row * A.pass;
+    const int step = (int)A.pass_div.div(kReadThreads);
+    if (row >= step) return;
+    for (int col = lane_col; col < A.cols; col += A.pass) {
+        const int which = col >= A.cols0 ? 1 : 0;
+        const CacheSide &S = A.side[which];
+        const uint32_t rest = (uint32_t)(col - (which ? A.cols0 : 0));
+        const uint32_t head = A.head_chunks[which].div(rest), ch = rest - head * A.head_chunks[which].d;
+        const uint8_t *codes = S.codes + (int64_t)head * S.head_stride + ch * 8;
+        const float *scales = S.scales + (int64_t)head * S.scale_head_stride + ch / 16;
+        uint8_t *dst = S.rows + 2 * (r0 * S.row_stride + (int64_t)head * S.row_head_stride + ch * 8);
+        for (int i0 = row; i0 < n; i0 += step * U) {
+            uint2 v[U];
+            float sc[U];
+            bool on[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t i = i0 + u * kReadThreads;
-            dst[u] = nullptr;
-            if (i < n) {
-                const uint32_t rl = A.per_row.div(i);
-                uint32_t rest = i - rl * A.per_row.d;
-                const int64_t page = s_page[rl];
-                if (page >= 0) {
-                    const int which = rest >= A.chunks[0] ? 1 : 0;
-                    rest -= which ? A.chunks[0] : 0u;
-                    const CacheSide &S = A.side[which];
-                    const uint32_t head = A.head_chunks[which].div(rest);
-                    const uint32_t ch = rest - head * A.head_chunks[which].d;
-                    const int64_t off = s_off[rl];
-                    v[u] = *reinterpret_cast<const uint4 *>(S.codes + page * S.page_stride + off * S.token_stride +
-                                                            (int64_t)head * S.head_stride + ch * 16);
-                    sc[u] = S.scales[page * S.scale_page_stride + off * S.scale_token_stride +
-                                     (int64_t)head * S.scale_head_stride + ch / 8];
-                    dst[u] = S.rows + 2 * ((r0 + rl) * S.row_stride + (int64_t)head * S.row_head_stride + ch * 16);
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * step;
+                on[u] = false;
+                if (i < n) {
+                    const SlotAt at = s_at[which][i];
+                    if (at.codes >= 0) {
+                        on[u] = true;
+                        v[u] = *reinterpret_cast<const uint2 *>(codes + at.codes);
+                        sc[u] = scales[at.scales];
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!dst[u]) continue;
-            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            uint32_t o[8];
-            const float2 s2 = make_float2(sc[u], sc[u]);
+            for (int u = 0; u < U; ++u) {
+                if (!on[u]) continue;
+                const uint32_t w[2] = {v[u].x, v[u].y};
+                uint32_t o[4];
+                const float2 s2 = make_float2(sc[u], sc[u]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                o[2 * j] = pack16<DT>(mul2(decode_e4m3x2((uint16_t)(w[j] & 0xFFFFu)), s2));
-                o[2 * j + 1] = pack16<DT>(mul2(decode_e4m3x2((uint16_t)(w[j] >> 16)), s2));
+                for (int j = 0; j < 2; ++j) {
+                    o[2 * j] = pack16<DT>(mul2(decode_e4m3x2((uint16_t)(w[j] & 0xFFFFu)), s2));
+                    o[2 * j + 1] = pack16<DT>(mul2(decode_e4m3x2((uint16_t)(w[j] >> 16)), s2));
+                }
+                *reinterpret_cast<uint4 *>(dst + 2 * (i0 + u * step) * S.row_stride) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            uint4 *d = reinterpret_cast<uint4 *>(dst[u]);
-            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
     }
 }

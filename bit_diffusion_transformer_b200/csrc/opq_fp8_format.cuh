@@ -6,14 +6,16 @@
 //   code  = the e4m3 number nearest 448 x / m, ties to even;  +-inf -> +-448, NaN -> NaN
 //   value = fl32(code * scale), rounded once more to the output's 16-bit type
 //
-// The code is exact for bf16 and fp16 inputs. 448 x / m is formed as y / a with y = (7/8) x and
-// a = m / 512, both exact in fp32 (at most 14 significant bits; a y that loses bits to fp32's
-// subnormal range is below 2^-50 of the block's largest and codes to 0 either way). The
-// correctly rounded fp32 quotient then rounds to the same e4m3 number as the real quotient: a
-// quotient that is not itself halfway between two codes differs from every such midpoint by at
-// least 2^-17 of its size (numerators of at most 14 bits, denominators of at most 11, midpoints
-// of 5), far more than fp32's 2^-24; and one that is halfway is an fp32 number, so it is
-// returned exactly and the conversion sees the tie.
+// The code is exact for bf16 and fp16 inputs, with one multiplication and one mask per value. The
+// encoder multiplies by (448 / m) (1 + 2^-21), formed in fp32, so that the fp32 product is the real
+// quotient 448 x / m times 1 + e with 0 < e < 2^-20, and clears the product's four lowest bits.
+//   - A quotient halfway between two codes has at most 5 significant bits; its product is above it
+//     by less than the 2^-19 that the mask removes, so the mask returns it exactly and the
+//     conversion sees the tie.
+//   - Any other quotient differs from every midpoint by at least 2^-16 of its size (448 x has at
+//     most 14 bits, m 11, a midpoint 5), which neither e nor the mask can bridge.
+// Infinities stay infinite and saturate to 448, NaN stays NaN. (Dividing, or correcting the product
+// by a residual, gives the same codes at two to four times the arithmetic.)
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,16 +29,11 @@ constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64
 
 enum { DT_BF16 = 0, DT_FP16 = 1 };
 
-// Per-block constants of the encoder.
-struct BlockScale {
-    float m, a, inv, scale;
-    __device__ __forceinline__ explicit BlockScale(float amax) {
-        m = fmaxf(amax, kFloor);
-        a = m * 0.001953125f;   // m / 512
-        inv = 1.0f / a;
-        scale = m / 448.0f;
-    }
-};
+// Per-block constants of m. Each takes a division, some ten instructions or more, so where lanes
+// hold several blocks each block's are formed by one lane and handed around.
+__device__ __forceinline__ float floored(float amax) { return fmaxf(amax, kFloor); }
+__device__ __forceinline__ float block_scale(float m) { return m / 448.0f; }
+__device__ __forceinline__ float block_mul(float m) { return (448.0f / m) * 1.000000476837158203125f; }   // 1 + 2^-21
 
 // Two fp32 operands per instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -98,9 +95,13 @@ __device__ __forceinline__ float unpack16_1(uint16_t v) {
 template <int DT>
 constexpr uint32_t kInfBits = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
 
-__device__ __forceinline__ uint32_t absmax8(const uint4 &v) {
+// the larger of two pairs of magnitudes' halves, per 16-bit half
+__device__ __forceinline__ uint32_t absmax8_pair(const uint4 &v) {
     const uint32_t k = 0x7FFF7FFFu;
-    const uint32_t w = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+    return __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+}
+__device__ __forceinline__ uint32_t absmax8(const uint4 &v) {
+    const uint32_t w = absmax8_pair(v);
     return max(w & 0xFFFFu, w >> 16);
 }
 // The same over the finite values only (the rare block that holds an infinity or a NaN).
@@ -121,26 +122,45 @@ __device__ __forceinline__ float bits_to_float(uint32_t b) {
     return unpack16_1<DT>((uint16_t)b);
 }
 
-// Eight values to eight codes. `clamp` (a block with non-finite values) takes infinities to +-m
-// first, keeping NaN; finite values are never above m.
+// Eight values to eight codes; mul = block_mul(m).
 template <int DT>
-__device__ __forceinline__ uint2 encode8(const uint4 &v, const BlockScale &s, bool clamp) {
+__device__ __forceinline__ uint2 encode8(const uint4 &v, float mul) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t c[4];
-    const float2 inv = make_float2(s.inv, s.inv), na = make_float2(-s.a, -s.a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 x = unpack16<DT>(w[i]);
-        if (clamp) {
-            x.x = x.x > s.m ? s.m : (x.x < -s.m ? -s.m : x.x);
-            x.y = x.y > s.m ? s.m : (x.y < -s.m ? -s.m : x.y);
-        }
-        const float2 y = mul2(x, make_float2(0.875f, 0.875f));
-        float2 q = mul2(y, inv);                       // within an ulp or two of y / a
-        q = fma2(fma2(q, na, y), inv, q);              // the residual is exact: correctly rounded
+        float2 q = mul2(unpack16<DT>(w[i]), make_float2(mul, mul));
+        q.x = __uint_as_float(__float_as_uint(q.x) & 0xFFFFFFF0u);
+        q.y = __uint_as_float(__float_as_uint(q.y) & 0xFFFFFFF0u);
         c[i] = cvt_e4m3x2(q);
     }
-    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410u), __byte_perm(c[2], c[3], 0x5410u));
+}
+
+// Largest magnitudes of U blocks, each held by LANES neighbouring lanes (eight values a lane):
+// two blocks' maxima travel in one word. A block with an infinity or a NaN takes its finite values'.
+template <int DT, int LANES, int U>
+__device__ __forceinline__ void block_maxima(const uint4 (&v)[U], uint32_t (&mx)[U]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < U; i += 2) {
+        const uint32_t a = absmax8(v[i]), b = i + 1 < U ? absmax8(v[i + 1 < U ? i + 1 : i]) : 0u;
+        uint32_t w = a | (b << 16);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, w, o));
+        mx[i] = w & 0xFFFFu;
+        if (i + 1 < U) mx[i + 1] = w >> 16;
+        top = __vmaxu2(top, w);
+    }
+    if (__any_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16) >= kInfBits<DT>)) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            uint32_t f = absmax8_finite<DT>(v[i]);
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) f = max(f, __shfl_xor_sync(0xFFFFFFFFu, f, o));
+            mx[i] = f;
+        }
+    }
 }
 
 // n / d and n % d for n < 2^31 by a multiplication (d is fixed per launch).

@@ -44,22 +44,20 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows_kernel(const 
         v[i] = make_uint4(0, 0, 0, 0);
         if (in_k && r < A.R) v[i] = *reinterpret_cast<const uint4 *>(A.x + (r * A.ldx + col) * 2);
     }
+    uint32_t mx[kQuantLoads];
+    block_maxima<DT, 16, kQuantLoads>(v, mx);
+    // lane l & 7 of a group forms the constants of the group's block l & 7
+    uint32_t own = mx[0];
+#pragma unroll
+    for (int i = 1; i < kQuantLoads; ++i) own = (l & 7) == i ? mx[i] : own;
+    const float om = floored(bits_to_float<DT>(own)), omul = block_mul(om);
+    if (l < 8) s_scale[g & 3][(g >> 2) + 4 * l] = block_scale(om);
+    uint8_t *dst = A.codes + (r0 + (g >> 2)) * A.ldc + col;
 #pragma unroll
     for (int i = 0; i < kQuantLoads; ++i) {
         const int rl = (g >> 2) + 4 * i;
-        uint32_t mx = absmax8(v[i]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        const bool wild = mx >= kInfBits<DT>;
-        if (__any_sync(0xFFFFFFFFu, wild)) {
-            mx = absmax8_finite<DT>(v[i]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        }
-        const BlockScale s(bits_to_float<DT>(mx));
-        if (l == 0) s_scale[g & 3][rl] = s.scale;
-        const uint2 c = encode8<DT>(v[i], s, wild);
-        if (in_k && r0 + rl < A.R) *reinterpret_cast<uint2 *>(A.codes + (r0 + rl) * A.ldc + col) = c;
+        const uint2 c = encode8<DT>(v[i], __shfl_sync(0xFFFFFFFFu, omul, i, 8));
+        if (in_k && r0 + rl < A.R) *reinterpret_cast<uint2 *>(dst + 4 * i * A.ldc) = c;
     }
     __syncthreads();
     if (threadIdx.x < 128) {
@@ -102,20 +100,19 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_blocks_kernel(cons
 #pragma unroll
     for (int i = 0; i < kQuantLoads; ++i) mx = max(mx, absmax8(v[i]));
     mx = block_max(mx);
-    const bool wild = mx >= kInfBits<DT>;      // the same for every thread of the CTA
-    if (wild) {
+    if (mx >= kInfBits<DT>) {      // the same for every thread of the CTA
         uint32_t fin = 0;
 #pragma unroll
         for (int i = 0; i < kQuantLoads; ++i) fin = max(fin, absmax8_finite<DT>(v[i]));
         __syncthreads();
         mx = block_max(fin);
     }
-    const BlockScale s(bits_to_float<DT>(mx));
-    if (threadIdx.x == 0) A.scales[(int64_t)kb * A.lds + rt] = s.scale;
+    const float m = floored(bits_to_float<DT>(mx)), mul = block_mul(m);
+    if (threadIdx.x == 0) A.scales[(int64_t)kb * A.lds + rt] = block_scale(m);
 #pragma unroll
     for (int i = 0; i < kQuantLoads; ++i) {
         const int64_t r = r0 + g + 16 * i;
-        if (in_k && r < A.R) *reinterpret_cast<uint2 *>(A.codes + r * A.ldc + col) = encode8<DT>(v[i], s, wild);
+        if (in_k && r < A.R) *reinterpret_cast<uint2 *>(A.codes + r * A.ldc + col) = encode8<DT>(v[i], mul);
     }
 }
 
