@@ -152,20 +152,43 @@ struct Fp8Plan {
     int split;   // narrow tiles: CTAs (a cluster) that share a tile's blocks
 };
 
+// The schedule, from the shape alone. Narrow tiles (64 rows of x or fewer, a tile's blocks shared by
+// a cluster) fit when the product is a stream of W or has few tiles; wide ones when it is bound by
+// the tensor cores. Above 32 rows of x the choice is by the time each would take, from these rates
+// (ns, measured at 3840 to 10240 columns with every SM busy):
+//   narrow 64          6000 + 760 per block of the longest range and round of 296 CTAs
+//   128 x 128, 1 CTA   2500 + per round of 148 tiles ( 500 + 345 per block)
+//   128 x 256, 1 CTA   2500 + per round of 148 tiles (1500 + 500 per block)
+//   256 x 256, a pair  2500 + per round of  74 tiles (1300 + 490 per block)
+// e.g. 256 x 1024 x 3840: narrow 8.8 us, 128 x 128 12.7; 256 x 3840 x 3840: 24 and 13;
+// 1089 x 3840 x 3840: 128 x 256 19.7, 128 x 128 25.2, pairs 34; 4096 x 10240 x 3840: pairs 147,
+// 128 x 256 153.
 Fp8Plan make_fp8_plan(int64_t M, int64_t N, int64_t K) {
-    Fp8Plan p{};
     const int64_t kblocks = (K + kBlock - 1) / kBlock;
-    if (M > 128) {
-        p.bn = 256;
-        p.cg = ((M + 127) / 128) * ((N + 255) / 256) > kSMs ? 2 : 1;
-        return p;
-    }
-    p.bx = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    const int64_t tiles = ((N + 127) / 128) * ((M + p.bx - 1) / p.bx);
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    Fp8Plan p{};
+    p.bx = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    // two CTAs per SM: as many ranges as fill them, of two blocks or more
+    const int64_t tiles = up(N, 128) * up(M, p.bx);
     int64_t s = 2 * kSMs / tiles;
     if (s > 8) s = 8;
     if (s > kblocks / 2) s = kblocks / 2;
-    p.split = s < 1 ? 1 : (int)s;
+    if (s < 1) s = 1;
+    p.split = (int)s;
+    if (M <= 32) return p;
+    int64_t best = 6000 + 760 * up(kblocks, s) * up(tiles * s, 2 * kSMs);
+    auto offer = [&](int cg, int bn, int64_t tile_ns, int64_t block_ns) {
+        const int64_t rounds = up(up(M, 128 * cg) * up(N, bn), kSMs / cg);
+        const int64_t ns = 2500 + rounds * (tile_ns + block_ns * kblocks);
+        if (ns < best) {
+            best = ns;
+            p.cg = cg;
+            p.bn = bn;
+        }
+    };
+    offer(1, 128, 500, 345);
+    offer(1, 256, 1500, 500);
+    offer(2, 256, 1300, 490);
     return p;
 }
 
@@ -179,16 +202,14 @@ opq_status run_linear(LinearArgs a, const void *x, int64_t ldx, const void *w, i
         if (p.bn == 256)
             return p.cg == 2 ? launch_wide<2, 256, DT>(a, x, ldx, w, ldw, K, stream)
                              : launch_wide<1, 256, DT>(a, x, ldx, w, ldw, K, stream);
-        return p.cg == 2 ? launch_wide<2, 128, DT>(a, x, ldx, w, ldw, K, stream)
-                         : launch_wide<1, 128, DT>(a, x, ldx, w, ldw, K, stream);
+        return launch_wide<1, 128, DT>(a, x, ldx, w, ldw, K, stream);
     }
     a.n_tiles = (a.N + 127) / 128;
     a.m_tiles = (a.M + p.bx - 1) / p.bx;
     switch (p.bx) {
         case 16: return launch_narrow<16, DT>(a, p.split, x, ldx, w, ldw, K, stream);
         case 32: return launch_narrow<32, DT>(a, p.split, x, ldx, w, ldw, K, stream);
-        case 64: return launch_narrow<64, DT>(a, p.split, x, ldx, w, ldw, K, stream);
-        default: return launch_narrow<128, DT>(a, p.split, x, ldx, w, ldw, K, stream);
+        default: return launch_narrow<64, DT>(a, p.split, x, ldx, w, ldw, K, stream);
     }
 }
 

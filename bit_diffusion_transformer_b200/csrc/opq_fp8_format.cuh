@@ -90,19 +90,30 @@ __device__ __forceinline__ float unpack16_1(uint16_t v) {
     return DT == DT_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
 }
 
-// The largest magnitude's bits of eight 16-bit values: magnitudes order as integers, and a
-// result at or above kInfBits says that the eight hold an infinity or a NaN.
+// Magnitudes order as integers; bits at or above kInfBits say that an infinity or a NaN is among
+// the values.
 template <int DT>
 constexpr uint32_t kInfBits = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
 
-// the larger of two pairs of magnitudes' halves, per 16-bit half
-__device__ __forceinline__ uint32_t absmax8_pair(const uint4 &v) {
-    const uint32_t k = 0x7FFF7FFFu;
-    return __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+// Per half: the larger magnitude (NaN if there is one) with some sign, one instruction.
+template <int DT>
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if (DT == DT_BF16)
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
+// of eight values: two candidates, in the halves
+template <int DT>
 __device__ __forceinline__ uint32_t absmax8(const uint4 &v) {
-    const uint32_t w = absmax8_pair(v);
-    return max(w & 0xFFFFu, w >> 16);
+    return absmax2<DT>(absmax2<DT>(v.x, v.y), absmax2<DT>(v.z, v.w));
+}
+// the larger of a word's halves, without its sign
+template <int DT>
+__device__ __forceinline__ uint32_t absmax_bits(uint32_t w) {
+    return absmax2<DT>(w, w >> 16) & 0x7FFFu;
 }
 // The same over the finite values only (the rare block that holds an infinity or a NaN).
 template <int DT>
@@ -144,15 +155,15 @@ __device__ __forceinline__ void block_maxima(const uint4 (&v)[U], uint32_t (&mx)
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < U; i += 2) {
-        const uint32_t a = absmax8(v[i]), b = i + 1 < U ? absmax8(v[i + 1 < U ? i + 1 : i]) : 0u;
-        uint32_t w = a | (b << 16);
+        const uint32_t a = absmax8<DT>(v[i]), b = absmax8<DT>(v[i + 1 < U ? i + 1 : i]);
+        uint32_t w = absmax2<DT>(__byte_perm(a, b, 0x5410u), __byte_perm(a, b, 0x7632u));   // a's, b's
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, w, o));
-        mx[i] = w & 0xFFFFu;
-        if (i + 1 < U) mx[i + 1] = w >> 16;
-        top = __vmaxu2(top, w);
+        for (int o = LANES / 2; o > 0; o >>= 1) w = absmax2<DT>(w, __shfl_xor_sync(0xFFFFFFFFu, w, o));
+        mx[i] = w & 0x7FFFu;
+        if (i + 1 < U) mx[i + 1] = (w >> 16) & 0x7FFFu;
+        top = absmax2<DT>(top, w);
     }
-    if (__any_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16) >= kInfBits<DT>)) {
+    if (__any_sync(0xFFFFFFFFu, absmax_bits<DT>(top) >= kInfBits<DT>)) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             uint32_t f = absmax8_finite<DT>(v[i]);

@@ -74,16 +74,23 @@ __device__ __forceinline__ float tanh_fast(float x) {
 }
 
 // The activations in fp32, as the packed-weight linears have them: one hardware tanh per output
-// (extra error at most about 2.5e-4 |v|).
-__device__ __forceinline__ float silu(float v) { return v * fmaf(0.5f, tanh_fast(0.5f * v), 0.5f); }
-__device__ __forceinline__ float gelu_tanh(float v) {
-    const float u = 0.7978845608028654f * fmaf(0.044715f * v, v * v, v);
-    const float h = 0.5f * v;
-    return fmaf(h, tanh_fast(u), h);
+// (extra error at most about 2.5e-4 |v|); two values at a time, which halves the instructions.
+//   SiLU  v / (1 + e^-v) = h + h tanh(h), h = v / 2
+//   GELU  h + h tanh(v (c + 0.044715 c v^2)), c = sqrt(2 / pi)
+__device__ __forceinline__ float2 tanh2(float2 v) { return make_float2(tanh_fast(v.x), tanh_fast(v.y)); }
+__device__ __forceinline__ float2 silu2(float2 v) {
+    const float2 h = mul2(v, make_float2(0.5f, 0.5f));
+    return fma2(h, tanh2(h), h);
+}
+__device__ __forceinline__ float2 gelu_tanh2(float2 v) {
+    constexpr float c = 0.7978845608028654f, c3 = 0.044715f * 0.7978845608028654f;
+    const float2 u = mul2(v, fma2(mul2(v, v), make_float2(c3, c3), make_float2(c, c)));
+    const float2 h = mul2(v, make_float2(0.5f, 0.5f));
+    return fma2(h, tanh2(u), h);
 }
 __device__ __forceinline__ float activate(float v, int act) {
-    if (act == ACT_SILU) return silu(v);
-    if (act == ACT_GELU_TANH) return gelu_tanh(v);
+    if (act == ACT_SILU) return silu2(make_float2(v, v)).x;
+    if (act == ACT_GELU_TANH) return gelu_tanh2(make_float2(v, v)).x;
     return v;
 }
 
@@ -154,6 +161,15 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// one arrival, by the lanes with `on` (a predicate, no branch)
+__device__ __forceinline__ void mbar_arrive_if(uint64_t *bar, bool on) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+        ::"r"(smem_u32(bar)), "r"((int)on) : "memory");
+}
+
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -164,17 +180,17 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
 // tile's blocks into S ranges so that the stream reaches every SM, and the ranges' fp32 sums meet
 // through the cluster's shared memory in rank order (no workspace, the same bits every run).
 //   warp 0       TMA producer: one 128-column block of W and of x per stage, 128-byte swizzle
-//   warp 1       TMEM allocation, the MMA issue (4 per block)
-//   warps 2..5   per block: sums out of TMEM, times the scales, into fp32 registers; the output
+//   warps 1, 2   TMEM allocation (warp 1), the MMA issue (4 per block), one block each in turn
+//   warps 4..7   per block: sums out of TMEM, times the scales, into fp32 registers; the output
 // ---------------------------------------------------------------------------------------------
 template <int BX>
 struct NarrowCfg {
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int X_BYTES = BX * 128;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = BX <= 32 ? 5 : (BX <= 64 ? 4 : 3);   // about 100 KiB: two CTAs per SM
-    static constexpr int NACC = BX <= 32 ? 4 : (BX <= 64 ? 4 : 2);     // blocks of sums in TMEM
-    static constexpr uint32_t TMEM_COLS = NACC * BX < 32 ? 32 : NACC * BX;
+    static constexpr int STAGES = BX <= 32 ? 5 : 4;                    // about 100 KiB: two CTAs per SM
+    static constexpr int NACC = 4;                                     // blocks of sums in TMEM
+    static constexpr uint32_t TMEM_COLS = NACC * BX;
     // scales of a chunk of blocks, 512 values (4 per epilogue thread), two chunks
     static constexpr int CHUNK = 512 / BX;
     static constexpr int OFF_SCALE = STAGES * STAGE;
@@ -182,18 +198,18 @@ struct NarrowCfg {
     static constexpr int NUM_BARS = 2 * STAGES + NACC + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;      // 1 KiB to align the stages
-    static constexpr int THREADS = 192;
+    static constexpr int THREADS = 256;
     static_assert(BX * 128 * 4 <= STAGES * STAGE, "the partial sums reuse the stages");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
     // one commit per block serves the producer (block i's stage) and the epilogue (block i's sums):
     // a stage's barrier completes again for block i + STAGES, whose MMAs wait for the epilogue to
     // have emptied the accumulator of block i + STAGES - NACC, so no completion is missed
-    static_assert(STAGES >= NACC, "done ring");
+    static_assert(STAGES >= NACC && NACC % 2 == 0, "done ring; an accumulator belongs to one issuer");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && 2 * TMEM_COLS <= 512, "two CTAs' TMEM per SM");
 };
 
 template <int BX, int DT>
-__global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
+__global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                       const __grid_constant__ LinearArgs A) {
     using C = NarrowCfg<BX>;
@@ -217,7 +233,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
         for (int s = 0; s < C::NACC; ++s) {
             mbar_init(&acc_empty[s], 4);
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, 2);
         fence_mbar_init();
         tma_prefetch_desc(&tmap_w);
         tma_prefetch_desc(&tmap_x);
@@ -254,32 +270,36 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
                 for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
                     wait8(&full[i % C::STAGES], (uint32_t)(i / C::STAGES & 1));
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(128, BX);
-            for (int b = b0, i = 0; b < b1; ++b, ++i) {
-                const int s = i % C::STAGES, a = i % C::NACC;
-                if (!wait8(&acc_empty[a], (uint32_t)(i / C::NACC & 1) ^ 1u)) break;
-                if (!wait8(&full[s], (uint32_t)(i / C::STAGES & 1))) break;
-                tc_fence_after();
-                const uint64_t wd = smem_desc_sw128(sbase + s * C::STAGE);
-                const uint64_t xd = smem_desc_sw128(sbase + s * C::STAGE + C::W_BYTES);
+    } else if (warp <= 2) {
+        // two warps issue in turn: a block's two waits, four MMAs and commit take one of them longer
+        // than its bytes take to arrive
+        constexpr uint32_t idesc = idesc_e4m3_f32(128, BX);
+        for (int i = warp - 1; i < b1 - b0; i += 2) {
+            const int s = i % C::STAGES, a = i % C::NACC;
+            if (!warp_wait8(&acc_empty[a], (uint32_t)(i / C::NACC & 1) ^ 1u)) break;
+            if (!warp_wait8(&full[s], (uint32_t)(i / C::STAGES & 1))) break;
+            tc_fence_after();
+            const uint64_t wd = smem_desc_sw128(sbase + s * C::STAGE);
+            const uint64_t xd = smem_desc_sw128(sbase + s * C::STAGE + C::W_BYTES);
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)     // 32 columns (32 bytes, 2 descriptor units) each
                     umma_f8_ss(tmem + a * BX, wd + 2 * k, xd + 2 * k, idesc, k > 0);
                 umma_commit(&done[s]);
             }
-            umma_commit(drain);
-            wait8(drain, 0);
+            __syncwarp();
         }
-    } else {
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        warp_wait8(drain, 0);
+    } else if (warp >= 4) {
         const int q = warp & 3;                      // TMEM lanes 32 q .. 32 q + 31
         const int e = q * 32 + lane;                 // this thread's output feature in the tile
         const int m0 = m_blk * BX, n = n_blk * 128 + e;
         float *sc = reinterpret_cast<float *>(smem + C::OFF_SCALE);
-        float acc[BX];
+        float2 acc[BX / 2];
 #pragma unroll
-        for (int j = 0; j < BX; ++j) acc[j] = 0.0f;
+        for (int j = 0; j < BX / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
         pdl_wait();
         // the scale of (block, row of x), times the block's scale of W: four per thread and chunk
         float pre[4];
@@ -301,6 +321,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
             named_bar(1, 128);
             if (c + C::CHUNK < b1) fetch(c + C::CHUNK);
             const int cend = c + C::CHUNK < b1 ? c + C::CHUNK : b1;
+#pragma unroll 1
             for (int b = c; b < cend; ++b) {
                 const int i = b - b0, a = i % C::NACC;
                 // a warp whose wait gave up skips the blocks that are left but still comes to every
@@ -308,33 +329,40 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
                 if (ok) ok = warp_wait8(&done[i % C::STAGES], (uint32_t)(i / C::STAGES & 1));
                 if (!ok) continue;
                 tc_fence_after();
-                const float *sb = buf + (b - c) * BX;
+                const float4 *sb = reinterpret_cast<const float4 *>(buf + (b - c) * BX);
+                constexpr int CH = BX < 32 ? BX : 32;      // columns in flight
+                const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + a * BX;
 #pragma unroll
-                for (int j0 = 0; j0 < BX; j0 += 16) {
-                    float t[16];
-                    tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + a * BX + j0, t);
+                for (int j0 = 0; j0 < BX; j0 += CH) {
+                    float t[CH];
+                    if (CH == 16)
+                        tmem_ld16(ta, *reinterpret_cast<float (*)[16]>(t));
+                    else
+                        tmem_ld32(ta + j0, t);
                     tmem_ld_wait();
+                    if (j0 + CH == BX) {
+                        tc_fence_before();
+                        mbar_arrive_if(&acc_empty[a], lane == 0);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 s2 = *reinterpret_cast<const float2 *>(sb + j0 + j);
-                        const float2 r = fma2(make_float2(t[j], t[j + 1]), s2, make_float2(acc[j0 + j], acc[j0 + j + 1]));
-                        acc[j0 + j] = r.x;
-                        acc[j0 + j + 1] = r.y;
+                    for (int j = 0; j < CH / 4; ++j) {
+                        const float4 s4 = sb[j0 / 4 + j];
+                        float2 &u = acc[j0 / 2 + 2 * j], &v = acc[j0 / 2 + 2 * j + 1];
+                        u = fma2(make_float2(t[4 * j], t[4 * j + 1]), make_float2(s4.x, s4.y), u);
+                        v = fma2(make_float2(t[4 * j + 2], t[4 * j + 3]), make_float2(s4.z, s4.w), v);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[a]);
             }
         }
         const int rows = A.M - m0 < BX ? A.M - m0 : BX;
-        const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(__ldg(A.bias + n)) : 0.0f;
         if (S == 1) {
+            const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(__ldg(A.bias + n)) : 0.0f;
             if (ok && n < A.N) {
 #pragma unroll
                 for (int j = 0; j < BX; ++j)
                     if (j < rows)
-                        A.y[(int64_t)(m0 + j) * A.ldy + n] = pack16_1<DT>(activate(acc[j] + bv, A.act));
+                        A.y[(int64_t)(m0 + j) * A.ldy + n] =
+                            pack16_1<DT>(activate((j & 1 ? acc[j / 2].y : acc[j / 2].x) + bv, A.act));
             }
         } else {
             // this range's sums into the stages (every copy has landed and every MMA has read them
@@ -342,7 +370,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
             float *part = reinterpret_cast<float *>(smem);
 #pragma unroll
             for (int j = 0; j < BX; ++j)
-                if (j < rows) part[j * 128 + e] = acc[j];
+                if (j < rows) part[j * 128 + e] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
         }
     }
 
@@ -350,14 +378,21 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS)
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        if (warp >= 2) {
-            const int e = (warp & 3) * 32 + lane;
+        {
+            // every warp takes part: two rows of x at a time
+            const int e = threadIdx.x & 127;
             const int m0 = m_blk * BX, n = n_blk * 128 + e;
             const int rows = A.M - m0 < BX ? A.M - m0 : BX;
             const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(__ldg(A.bias + n)) : 0.0f;
-            for (int j = rank; j < rows; j += S) {
-                float v = 0.0f;
-                for (int r = 0; r < S; ++r) v += ld_cluster_f32(mapa(sbase + (uint32_t)(j * 128 + e) * 4u, (uint32_t)r));
+            for (int j = rank + S * (threadIdx.x >> 7); j < rows; j += 2 * S) {
+                // all ranges' sums asked for at once, added in rank order
+                const uint32_t at = sbase + (uint32_t)(j * 128 + e) * 4u;
+                float p[8], v = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) p[r] = r < S ? ld_cluster_f32(mapa(at, (uint32_t)r)) : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < S) v += p[r];
                 if (n < A.N) A.y[(int64_t)(m0 + j) * A.ldy + n] = pack16_1<DT>(activate(v + bv, A.act));
             }
         }
@@ -759,25 +794,15 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
                     const uint4 w = reinterpret_cast<const uint4 *>(bias_s)[j];
                     const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 bv = unpack16<DT>(w4[i]);
-                        acc[4 * j + i].x += bv.x;
-                        acc[4 * j + i].y += bv.y;
-                    }
+                    for (int i = 0; i < 4; ++i) acc[4 * j + i] = fma2(acc[4 * j + i], make_float2(1.0f, 1.0f), unpack16<DT>(w4[i]));
                 }
             }
             if (A.act == ACT_SILU) {
 #pragma unroll
-                for (int j = 0; j < C::HALF / 2; ++j) {
-                    acc[j].x = silu(acc[j].x);
-                    acc[j].y = silu(acc[j].y);
-                }
+                for (int j = 0; j < C::HALF / 2; ++j) acc[j] = silu2(acc[j]);
             } else if (A.act == ACT_GELU_TANH) {
 #pragma unroll
-                for (int j = 0; j < C::HALF / 2; ++j) {
-                    acc[j].x = gelu_tanh(acc[j].x);
-                    acc[j].y = gelu_tanh(acc[j].y);
-                }
+                for (int j = 0; j < C::HALF / 2; ++j) acc[j] = gelu_tanh2(acc[j]);
             }
 #pragma unroll
             for (int rd = 0; rd < C::ROUNDS; ++rd) {

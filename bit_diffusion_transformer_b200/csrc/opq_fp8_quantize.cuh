@@ -37,12 +37,14 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows_kernel(const 
     const int col = kb * kBlock + l * 8;
     const bool in_k = col < A.K;       // K % 32 == 0: a lane's eight columns are in or out together
     opqdev::pdl_wait();
+    const int left = in_k ? (int)(A.R - r0 < 32 ? A.R - r0 : 32) - (g >> 2) : 0;   // rows from this lane's first
     uint4 v[kQuantLoads];
+    const uint8_t *src = A.x + ((r0 + (g >> 2)) * A.ldx + col) * 2;
+    const int64_t sstep = 8 * A.ldx, dstep = 4 * A.ldc;
 #pragma unroll
-    for (int i = 0; i < kQuantLoads; ++i) {
-        const int64_t r = r0 + (g >> 2) + 4 * i;
+    for (int i = 0; i < kQuantLoads; ++i, src += sstep) {
         v[i] = make_uint4(0, 0, 0, 0);
-        if (in_k && r < A.R) v[i] = *reinterpret_cast<const uint4 *>(A.x + (r * A.ldx + col) * 2);
+        if (4 * i < left) v[i] = *reinterpret_cast<const uint4 *>(src);
     }
     uint32_t mx[kQuantLoads];
     block_maxima<DT, 16, kQuantLoads>(v, mx);
@@ -54,10 +56,9 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows_kernel(const 
     if (l < 8) s_scale[g & 3][(g >> 2) + 4 * l] = block_scale(om);
     uint8_t *dst = A.codes + (r0 + (g >> 2)) * A.ldc + col;
 #pragma unroll
-    for (int i = 0; i < kQuantLoads; ++i) {
-        const int rl = (g >> 2) + 4 * i;
+    for (int i = 0; i < kQuantLoads; ++i, dst += dstep) {
         const uint2 c = encode8<DT>(v[i], __shfl_sync(0xFFFFFFFFu, omul, i, 8));
-        if (in_k && r0 + rl < A.R) *reinterpret_cast<uint2 *>(dst + 4 * i * A.ldc) = c;
+        if (4 * i < left) *reinterpret_cast<uint2 *>(dst) = c;
     }
     __syncthreads();
     if (threadIdx.x < 128) {
@@ -80,12 +81,14 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_blocks_kernel(cons
     const int col = kb * kBlock + l * 8;
     const bool in_k = col < A.K;
     opqdev::pdl_wait();
+    const int left = in_k ? (int)(A.R - r0 < kBlock ? A.R - r0 : kBlock) - g : 0;   // rows from this lane's first
     uint4 v[kQuantLoads];
+    const uint8_t *src = A.x + ((r0 + g) * A.ldx + col) * 2;
+    const int64_t sstep = 32 * A.ldx, dstep = 16 * A.ldc;
 #pragma unroll
-    for (int i = 0; i < kQuantLoads; ++i) {
-        const int64_t r = r0 + g + 16 * i;
+    for (int i = 0; i < kQuantLoads; ++i, src += sstep) {
         v[i] = make_uint4(0, 0, 0, 0);
-        if (in_k && r < A.R) v[i] = *reinterpret_cast<const uint4 *>(A.x + (r * A.ldx + col) * 2);
+        if (16 * i < left) v[i] = *reinterpret_cast<const uint4 *>(src);
     }
     auto block_max = [&](uint32_t mx) {
         mx = __reduce_max_sync(0xFFFFFFFFu, mx);
@@ -98,8 +101,8 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_blocks_kernel(cons
     };
     uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < kQuantLoads; ++i) mx = max(mx, absmax8(v[i]));
-    mx = block_max(mx);
+    for (int i = 0; i < kQuantLoads; ++i) mx = absmax2<DT>(mx, absmax8<DT>(v[i]));
+    mx = block_max(absmax_bits<DT>(mx));
     if (mx >= kInfBits<DT>) {      // the same for every thread of the CTA
         uint32_t fin = 0;
 #pragma unroll
@@ -109,11 +112,10 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_blocks_kernel(cons
     }
     const float m = floored(bits_to_float<DT>(mx)), mul = block_mul(m);
     if (threadIdx.x == 0) A.scales[(int64_t)kb * A.lds + rt] = block_scale(m);
+    uint8_t *dst = A.codes + (r0 + g) * A.ldc + col;
 #pragma unroll
-    for (int i = 0; i < kQuantLoads; ++i) {
-        const int64_t r = r0 + g + 16 * i;
-        if (in_k && r < A.R) *reinterpret_cast<uint2 *>(A.codes + r * A.ldc + col) = encode8<DT>(v[i], mul);
-    }
+    for (int i = 0; i < kQuantLoads; ++i, dst += dstep)
+        if (16 * i < left) *reinterpret_cast<uint2 *>(dst) = encode8<DT>(v[i], mul);
 }
 
 }  // namespace opqfp8
