@@ -1,6 +1,6 @@
 // opq_capi.cu — the C ABI of libopq.so (declared in include/opq.h): argument
 // validation, the alpha-dependent tables, TMA descriptors, kernel selection and
-// launches. The whole library is this one translation unit.
+// launches of the OPQ format (the 8-bit format's are in opq_fp8.cu).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

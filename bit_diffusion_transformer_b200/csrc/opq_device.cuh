@@ -9,8 +9,8 @@
 namespace opqdev {
 
 // Device-side error word (bitmask of OPQ_DEVERR_*), read and cleared by
-// opq_device_error(). The library is a single translation unit, so the
-// definition lives here.
+// opq_device_error(). Device symbols belong to their translation unit: opq_capi.cu and
+// opq_fp8.cu each have their own, and opq_device_error() reads both.
 __device__ uint32_t g_error = 0;
 constexpr uint32_t kErrWaitTimeout = 1u;
 constexpr uint32_t kErrSmemAlign = 2u;     // dynamic shared memory not on the 1 KiB boundary

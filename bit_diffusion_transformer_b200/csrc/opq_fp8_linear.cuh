@@ -179,9 +179,15 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
 // of x. For few rows of x the product is bound by streaming W once; a cluster of S CTAs cuts the
 // tile's blocks into S ranges so that the stream reaches every SM, and the ranges' fp32 sums meet
 // through the cluster's shared memory in rank order (no workspace, the same bits every run).
+// Measured: 1 x 11520 x 3840 10.4 us (44 MB, 0.64 of the copy bandwidth), 32 x 11520 x 3840 12.8,
+// 37 x 3840 x 10240 12.9; one launch costs about 3 us before and after its stream (barriers, the first
+// copies' latency, the cluster's exchange), and a block is a chain of hand-overs (copy, MMA, sums) of
+// about 0.4 us per CTA, which two CTAs per SM and two issuing warps overlap. Reading W straight into
+// mma.sync operands instead started faster (2.1 us for 512 x 1024 against 2.9) but was bound by its
+// conversions on real layers (13.5 us).
 //   warp 0       TMA producer: one 128-column block of W and of x per stage, 128-byte swizzle
 //   warps 1, 2   TMEM allocation (warp 1), the MMA issue (4 per block), one block each in turn
-//   warps 4..7   per block: sums out of TMEM, times the scales, into fp32 registers; the output
+//   warps 4..    per block: sums out of TMEM, times the scales, into fp32 registers; the output
 // ---------------------------------------------------------------------------------------------
 template <int BX>
 struct NarrowCfg {
@@ -198,7 +204,10 @@ struct NarrowCfg {
     static constexpr int NUM_BARS = 2 * STAGES + NACC + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;      // 1 KiB to align the stages
-    static constexpr int THREADS = 256;
+    // EP warps per TMEM lane quarter, CW rows of x (columns of sums) each, so that a block is one TMEM
+    // load per warp (37 x 3840 x 10240: 12.9 us; one warp for all 64 columns 13.7)
+    static constexpr int EP = BX >= 32 ? 2 : 1, CW = BX / EP;
+    static constexpr int THREADS = 128 + 128 * EP;
     static_assert(BX * 128 * 4 <= STAGES * STAGE, "the partial sums reuse the stages");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
     // one commit per block serves the producer (block i's stage) and the epilogue (block i's sums):
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
             mbar_init(&done[s], 1);
         }
         for (int s = 0; s < C::NACC; ++s) {
-            mbar_init(&acc_empty[s], 4);
+            mbar_init(&acc_empty[s], 4 * C::EP);
         }
         mbar_init(drain, 2);
         fence_mbar_init();
@@ -295,18 +304,21 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
     } else if (warp >= 4) {
         const int q = warp & 3;                      // TMEM lanes 32 q .. 32 q + 31
         const int e = q * 32 + lane;                 // this thread's output feature in the tile
+        const int x0 = ((warp - 4) >> 2) * C::CW;    // and its first row of x
         const int m0 = m_blk * BX, n = n_blk * 128 + e;
+        const int et = threadIdx.x - 128;
         float *sc = reinterpret_cast<float *>(smem + C::OFF_SCALE);
-        float2 acc[BX / 2];
+        float2 acc[C::CW / 2];
 #pragma unroll
-        for (int j = 0; j < BX / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+        for (int j = 0; j < C::CW / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
         pdl_wait();
-        // the scale of (block, row of x), times the block's scale of W: four per thread and chunk
-        float pre[4];
+        // the scale of (block, row of x), times the block's scale of W: PER per thread and chunk
+        constexpr int PER = 4 / C::EP, EPT = 128 * C::EP;
+        float pre[PER];
         auto fetch = [&](int c) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int idx = u * 128 + e, b = c + idx / BX, m = m0 + idx % BX;
+            for (int u = 0; u < PER; ++u) {
+                const int idx = u * EPT + et, b = c + idx / BX, m = m0 + idx % BX;
                 pre[u] = 0.0f;
                 if (b < b1 && m < A.M)
                     pre[u] = __ldg(A.xs + (int64_t)b * A.ld_xs + m) * __ldg(A.ws + (int64_t)b * A.ld_ws + n_blk);
@@ -317,8 +329,8 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
         for (int c = b0, ci = 0; c < b1; c += C::CHUNK, ++ci) {
             float *buf = sc + (ci & 1) * 512;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) buf[u * 128 + e] = pre[u];
-            named_bar(1, 128);
+            for (int u = 0; u < PER; ++u) buf[u * EPT + et] = pre[u];
+            named_bar(1, EPT);
             if (c + C::CHUNK < b1) fetch(c + C::CHUNK);
             const int cend = c + C::CHUNK < b1 ? c + C::CHUNK : b1;
 #pragma unroll 1
@@ -329,28 +341,21 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
                 if (ok) ok = warp_wait8(&done[i % C::STAGES], (uint32_t)(i / C::STAGES & 1));
                 if (!ok) continue;
                 tc_fence_after();
-                const float4 *sb = reinterpret_cast<const float4 *>(buf + (b - c) * BX);
-                constexpr int CH = BX < 32 ? BX : 32;      // columns in flight
-                const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + a * BX;
+                const float4 *sb = reinterpret_cast<const float4 *>(buf + (b - c) * BX + x0);
+                const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + a * BX + x0;
+                float t[C::CW];
+                if (C::CW == 16)
+                    tmem_ld16(ta, *reinterpret_cast<float (*)[16]>(t));
+                else
+                    tmem_ld32(ta, t);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive_if(&acc_empty[a], lane == 0);
 #pragma unroll
-                for (int j0 = 0; j0 < BX; j0 += CH) {
-                    float t[CH];
-                    if (CH == 16)
-                        tmem_ld16(ta, *reinterpret_cast<float (*)[16]>(t));
-                    else
-                        tmem_ld32(ta + j0, t);
-                    tmem_ld_wait();
-                    if (j0 + CH == BX) {
-                        tc_fence_before();
-                        mbar_arrive_if(&acc_empty[a], lane == 0);
-                    }
-#pragma unroll
-                    for (int j = 0; j < CH / 4; ++j) {
-                        const float4 s4 = sb[j0 / 4 + j];
-                        float2 &u = acc[j0 / 2 + 2 * j], &v = acc[j0 / 2 + 2 * j + 1];
-                        u = fma2(make_float2(t[4 * j], t[4 * j + 1]), make_float2(s4.x, s4.y), u);
-                        v = fma2(make_float2(t[4 * j + 2], t[4 * j + 3]), make_float2(s4.z, s4.w), v);
-                    }
+                for (int j = 0; j < C::CW / 4; ++j) {
+                    const float4 s4 = sb[j];
+                    acc[2 * j] = fma2(make_float2(t[4 * j], t[4 * j + 1]), make_float2(s4.x, s4.y), acc[2 * j]);
+                    acc[2 * j + 1] = fma2(make_float2(t[4 * j + 2], t[4 * j + 3]), make_float2(s4.z, s4.w), acc[2 * j + 1]);
                 }
             }
         }
@@ -359,9 +364,9 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
             const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(__ldg(A.bias + n)) : 0.0f;
             if (ok && n < A.N) {
 #pragma unroll
-                for (int j = 0; j < BX; ++j)
-                    if (j < rows)
-                        A.y[(int64_t)(m0 + j) * A.ldy + n] =
+                for (int j = 0; j < C::CW; ++j)
+                    if (x0 + j < rows)
+                        A.y[(int64_t)(m0 + x0 + j) * A.ldy + n] =
                             pack16_1<DT>(activate((j & 1 ? acc[j / 2].y : acc[j / 2].x) + bv, A.act));
             }
         } else {
@@ -369,8 +374,8 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
             // once the last block's sums are complete), [row of x][feature]
             float *part = reinterpret_cast<float *>(smem);
 #pragma unroll
-            for (int j = 0; j < BX; ++j)
-                if (j < rows) part[j * 128 + e] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+            for (int j = 0; j < C::CW; ++j)
+                if (x0 + j < rows) part[(x0 + j) * 128 + e] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
         }
     }
 
@@ -379,12 +384,12 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
         cluster_arrive();
         cluster_wait();
         {
-            // every warp takes part: two rows of x at a time
+            // every warp takes part: a row of x per 128 threads
             const int e = threadIdx.x & 127;
             const int m0 = m_blk * BX, n = n_blk * 128 + e;
             const int rows = A.M - m0 < BX ? A.M - m0 : BX;
             const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(__ldg(A.bias + n)) : 0.0f;
-            for (int j = rank + S * (threadIdx.x >> 7); j < rows; j += 2 * S) {
+            for (int j = rank + S * (threadIdx.x >> 7); j < rows; j += S * (C::THREADS / 128)) {
                 // all ranges' sums asked for at once, added in rank order
                 const uint32_t at = sbase + (uint32_t)(j * 128 + e) * 4u;
                 float p[8], v = 0.0f;
@@ -417,6 +422,12 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
 //                Each block's sums leave TMEM (two accumulators in turn, so the tensor pipe runs
 //                on) and are added times sx[row] sw[block of W]: one scalar per thread and block.
 //                The finished rows go through shared memory and leave by TMA.
+// Measured: 4096 x 10240 x 3840 146 us (2200 TFLOP/s, 0.67 of twice the bf16 rate), with GELU 158;
+// 1089 x 3840 x 3840 19.4 us on single CTAs. A block is 512 cycles of MMA and takes about 850: the
+// sums of two blocks fill TMEM, so block i + 2 waits for block i's trip through the epilogue (commit to
+// wait 200 cycles, loads 250, hand-back 250), and the epilogue's own work per block is about 560.
+// Leaving out any one of copies, TMEM loads, additions or scales gains 4 to 15%: nothing alone
+// bounds it. Halving the tile's MMAs (N = 128, a barrier per half) was 9% slower on pairs.
 // ---------------------------------------------------------------------------------------------
 template <int CG, int BN>
 struct WideCfg {
