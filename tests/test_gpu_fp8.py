@@ -148,6 +148,56 @@ def test_linear_larger(M, N, K):
     check_linear(operands(M, N, K, seed=5))
 
 
+@pytest.mark.parametrize("M,N,K,act", [
+    # narrow tiles: one to eight ranges of blocks, with blocks left over, several row tiles
+    (7, 40000, 384, "none"), (20, 18000, 1152, "silu"), (60, 6500, 2720, "none"), (16, 4600, 3104, "gelu_tanh"),
+    (90, 2100, 2912, "none"), (130, 500, 4000, "silu"), (9, 129, 2048, "none"),
+    # whole tiles on single CTAs and on pairs: one round and several, rows that TMA cannot store
+    (700, 2001, 1024, "gelu_tanh"), (1000, 4104, 416, "none"), (2300, 4100, 288, "silu"), (2600, 5001, 416, "gelu_tanh"),
+    (4400, 2568, 160, "none")])
+def test_linear_schedules(M, N, K, act):
+    check_linear(operands(M, N, K, seed=M), randn(N, seed=3), act)
+
+
+def test_linear_outputs_past_31_bits():
+    """2.2 G outputs: the last rows are at offsets past 2^31 elements."""
+    M, N, K = 70016, 32000, 32
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
+    w = torch.empty((N, K), dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(2))
+    ops = (*opq.fp8_quantize(x), *opq.fp8_quantize(w, 128))
+    y = opq.fp8_linear(*ops)
+    assert y.numel() > 1 << 31
+    xc, xs, wc, ws = [t.cpu() for t in ops]
+    for rows in (slice(0, 40), slice(M // 2, M // 2 + 40), slice(M - 40, M)):
+        want, B, v = ref.linear(xc[rows], xs[:, rows], wc, ws)
+        tol = ref.linear_tolerance(want, B, v, None, "none", torch.bfloat16, K)
+        assert bool(((y[rows].cpu().double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_past_31_bits(block_rows):
+    R, K = 66000, 32768
+    x = torch.empty((R, K), dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
+    assert x.numel() > 1 << 31
+    codes, scales = opq.fp8_quantize(x, block_rows)
+    for r0 in (0, 65920):                      # the last one starts a 128-row block and ends the matrix
+        c, s = ref.quantize(x[r0:r0 + 128, -256:].cpu(), block_rows)
+        same_codes(codes[r0:r0 + 128, -256:], c)
+        same_scales(scales[-2:, r0 // block_rows:r0 // block_rows + s.shape[1]], s)
+
+
+def test_linear_after_a_changed_wait_limit():
+    """The bounded waits' limit reaches these kernels too, and no wait of a healthy call comes near it."""
+    ops = operands(300, 700, 1024, seed=2)
+    try:
+        opq.set_wait_limit_ns(50_000_000)
+        check_linear(ops)
+        assert opq.device_error() == 0
+    finally:
+        opq.set_wait_limit_ns(0)
+    check_linear(ops)
+
+
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
 @pytest.mark.parametrize("with_bias", [False, True])
