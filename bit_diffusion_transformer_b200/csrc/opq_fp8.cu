@@ -154,9 +154,10 @@ struct Fp8Plan {
 
 // The schedule, from the shape alone. Narrow tiles (64 rows of x or fewer, a tile's blocks shared by
 // a cluster) fit when the product is a stream of W or has few tiles; wide ones when it is bound by
-// the tensor cores. Above 32 rows of x the choice is by the time each would take, from these rates
-// (ns, measured at 3840 to 10240 columns with every SM busy):
-//   narrow 64          6000 + 760 per block of the longest range and round of 296 CTAs
+// the tensor cores. Above 32 rows of x, or where narrow tiles take several rounds, the choice is by
+// the time each would take, from these rates (ns, measured at 3840 to 10240 columns with every SM busy):
+//   narrow             per round of 296 CTAs 6000 + 760 per block of the longest range (440 for 16
+//                      rows, 680 for 32)
 //   128 x 128, 1 CTA   2500 + per round of 148 tiles ( 500 + 345 per block)
 //   128 x 256, 1 CTA   2500 + per round of 148 tiles (1500 + 500 per block)
 //   256 x 256, a pair  2500 + per round of  74 tiles (1300 + 490 per block)
@@ -175,8 +176,9 @@ Fp8Plan make_fp8_plan(int64_t M, int64_t N, int64_t K) {
     if (s > kblocks / 2) s = kblocks / 2;
     if (s < 1) s = 1;
     p.split = (int)s;
-    if (M <= 32) return p;
-    int64_t best = 6000 + 760 * up(kblocks, s) * up(tiles * s, 2 * kSMs);
+    const int64_t rounds = up(tiles * s, 2 * kSMs);
+    if (M <= 32 && rounds == 1) return p;
+    int64_t best = rounds * (6000 + (p.bx == 16 ? 440 : p.bx == 32 ? 680 : 760) * up(kblocks, s));
     auto offer = [&](int cg, int bn, int64_t tile_ns, int64_t block_ns) {
         const int64_t rounds = up(up(M, 128 * cg) * up(N, bn), kSMs / cg);
         const int64_t ns = 2500 + rounds * (tile_ns + block_ns * kblocks);

@@ -98,7 +98,8 @@ def fp8_cache_read(cache, page_table: torch.Tensor, cu_rows: torch.Tensor, rows:
     ``page_table`` int32 [B, W]: the pages of each sequence in order. ``cu_rows`` int32 [B + 1]:
     sequence b's tokens go to rows cu_rows[b] .. cu_rows[b + 1] - 1, from position ``starts``[b]
     (int32 [B]; None: 0) on. ``rows`` is the number of output rows (cu_rows[B] or more, on the
-    host); rows that no sequence holds stay as they were (unset in a new output). ``out`` = (k, v) to write into,
-    any strides with contiguous channels. A cache of keys alone, (codes, scales), gives (k,).
-    Pages out of range leave their rows unwritten and are reported by device_error()."""
+    host); rows that no sequence holds stay as they were (unset in a new output). ``out`` = (k, v)
+    to write into, any strides with contiguous channels. A cache of keys alone, (codes, scales),
+    gives (k,). Pages out of range leave their rows unwritten and are reported by device_error()
+    (DEVERR_INDEX)."""
     return (_ext or _load()).cache_read(cache, page_table, cu_rows, rows, starts, dtype, out)
