@@ -59,7 +59,7 @@ def _link_ext(obj: str, out: str):
     import torch
     tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
     subprocess.check_call(["g++", "-shared", "-o", out, obj, "-L", HERE, "-lopq", "-Wl,-rpath,$ORIGIN", "-L", tlib,
-                           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+                           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
