@@ -170,6 +170,11 @@ __device__ __forceinline__ void mbar_arrive_if(uint64_t *bar, bool on) {
         ::"r"(smem_u32(bar)), "r"((int)on) : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(c0), "r"(c1)
+                 : "memory");
+}
+
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -179,7 +184,7 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
 // of x. For few rows of x the product is bound by streaming W once; a cluster of S CTAs cuts the
 // tile's blocks into S ranges so that the stream reaches every SM, and the ranges' fp32 sums meet
 // through the cluster's shared memory in rank order (no workspace, the same bits every run).
-// Measured: 1 x 11520 x 3840 10.4 us (44 MB, 0.64 of the copy bandwidth), 32 x 11520 x 3840 12.8,
+// Measured: 1 x 11520 x 3840 10.0 us (44 MB, 0.67 of the copy bandwidth), 32 x 11520 x 3840 12.2,
 // 37 x 3840 x 10240 12.9; one launch costs about 3 us before and after its stream (barriers, the first
 // copies' latency, the cluster's exchange), and a block is a chain of hand-overs (copy, MMA, sums) of
 // about 0.4 us per CTA, which two CTAs per SM and two issuing warps overlap. Reading W straight into
@@ -194,7 +199,11 @@ struct NarrowCfg {
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int X_BYTES = BX * 128;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = BX <= 32 ? 5 : 4;                    // about 100 KiB: two CTAs per SM
+    static constexpr int STAGES = 4;                                   // three CTAs per SM at BX = 16
+    // blocks of W asked for ahead of the previous kernel's end: as many as the first copies take
+    // (1 x 3840 x 3840 5.98 -> 5.75 us, 64 x 3840 x 3840 9.67 -> 9.35; ten blocks gain nothing more and
+    // cost 37 x 3840 x 10240 1.5 us)
+    static constexpr int AHEAD = STAGES;
     static constexpr int NACC = 4;                                     // blocks of sums in TMEM
     static constexpr uint32_t TMEM_COLS = NACC * BX;
     // scales of a chunk of blocks, 512 values (4 per epilogue thread), two chunks
@@ -263,6 +272,10 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
 
     if (warp == 0) {
         if (lane == 0) {
+            // The range's first blocks of W start for L2 before the previous kernel of the stream has
+            // ended. A prefetch returns nothing, so it cannot return what that kernel still changes:
+            // its writes and the copies below meet in L2.
+            for (int b = b0; b < b1 && b < b0 + C::AHEAD; ++b) tma_prefetch_2d(&tmap_w, b * kBlock, n_blk * 128);
             pdl_wait();
             bool ok = true;
             int issued = 0;
