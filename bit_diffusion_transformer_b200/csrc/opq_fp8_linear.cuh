@@ -243,7 +243,6 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        pdl_launch_dependents();
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&done[s], 1);
@@ -256,9 +255,13 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
         tma_prefetch_desc(&tmap_w);
         tma_prefetch_desc(&tmap_x);
     }
+    // Two kernels' CTAs can share an SM here, so that tensor memory must not close a circle of waits:
+    // the next kernel may start only when this CTA has its own, and this CTA gives it back before it
+    // waits for its cluster.
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
+        if (lane == 0) pdl_launch_dependents();
     }
     tc_fence_before();
     __syncthreads();
@@ -292,7 +295,9 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
                 for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
                     wait8(&full[i % C::STAGES], (uint32_t)(i / C::STAGES & 1));
         }
-    } else if (warp <= 2) {
+    }
+
+    if (warp == 1 || warp == 2) {
         // two warps issue in turn: a block's two waits, four MMAs and commit take one of them longer
         // than its bytes take to arrive
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BX);
@@ -392,6 +397,10 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
         }
     }
 
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
     if (S > 1) {
         __syncwarp();
         cluster_arrive();
@@ -418,9 +427,6 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
         cluster_arrive();   // no CTA leaves while another still reads its sums
         cluster_wait();
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -474,7 +480,7 @@ struct WideCfg {
     // warpgroup gives up what they take. The launch checks that the kernel was built for REG_LAUNCH.
     static constexpr int REG_LAUNCH = 168, REG_EPI = 224, REG_PROD = 3 * REG_LAUNCH - 2 * REG_EPI;
     static_assert(THREADS * REG_LAUNCH <= 65536 && REG_PROD % 8 == 0 && REG_PROD >= 40, "register split");
-    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(SMEM <= 232448 && SMEM > 200 * 1024, "shared memory: one CTA per SM");
     static_assert(STAGES >= NACC && RING >= STAGES + NACC && LAG < STAGES, "done ring (as for the narrow tiles)");
     static_assert(STAGE % 1024 == 0 && HALF % 64 == 0 && TMEM_COLS <= 512, "layout");
 };
@@ -607,6 +613,8 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
         return;
     }
 
+    // (the next kernel may start at once: with this CTA's shared memory in use, no other CTA that
+    // takes tensor memory fits on the SM, so none can hold it while this one still asks)
     if (threadIdx.x == 0) {
         pdl_launch_dependents();
         for (int s = 0; s < C::STAGES; ++s) {
