@@ -769,6 +769,7 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
             if (A.bias != nullptr) {
                 __syncwarp();
                 for (int j = lane; j < C::HALF; j += 32) bias_s[j] = n0 + j < A.N ? __ldg(A.bias + n0 + j) : (uint16_t)0;
+                __syncwarp();      // every lane reads what all lanes stored
             }
             float2 acc[C::HALF / 2];
 #pragma unroll

@@ -1,0 +1,48 @@
+"""The 8-bit linear's tile kinds and epilogues on operands quantized on the GPU (whose codes
+test_gpu_fp8.py holds to the definition), against float64 products on the GPU within the derived
+tolerance of fp8_reference.linear_tolerance."""
+import pytest
+import torch
+
+import bit_diffusion_transformer_b200 as opq
+import fp8_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    torch.cuda.synchronize()
+    assert opq.device_error() == 0
+
+
+def gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+def normal(*shape, seed=0, scale=1.0, dtype=torch.bfloat16):
+    return (torch.randn(*shape, generator=gen(seed), device=DEV) * scale).to(dtype)
+
+
+def operands(M, N, K, seed=0):
+    return (*opq.fp8_quantize(normal(M, K, seed=seed)), *opq.fp8_quantize(normal(N, K, seed=seed + 1, scale=0.02), 128))
+
+
+def check(ops, bias=None, act="none", dtype=torch.bfloat16):
+    y = opq.fp8_linear(*ops, bias=bias, act=act, dtype=dtype)
+    want, B, v = ref.linear(*ops, bias, act)
+    tol = ref.linear_tolerance(want, B, v, bias, act, dtype, ops[0].shape[1])
+    err = (y.double() - want).abs()
+    assert y.dtype == dtype and bool(torch.isfinite(y).all())
+    assert bool((err <= tol).all()), f"{int((err > tol).sum())} of {err.numel()} out, worst {float((err / tol).max()):.3g}"
+
+
+@pytest.mark.parametrize("M,N", [(1000, 4104), (2600, 5001)])
+def test_bias_of_each_tile_over_one_block(M, N):
+    """One block per tile: nothing but the epilogue's own barriers stands between a tile's bias, stored
+    by all lanes of a warp, and its readers. Several tiles per CTA, each with a bias of its own."""
+    bias = torch.arange(N, device=DEV).remainder(509).sub(254).to(torch.bfloat16)
+    for K in (96, 128):
+        check(operands(M, N, K, seed=K), bias)
