@@ -5,6 +5,9 @@
 // The inner sums run on the tensor cores (tcgen05 kind::f8f6f4, e4m3 operands from shared memory,
 // fp32 accumulators in TMEM). The scales are any fp32 numbers, so each 128-column block's sums
 // leave TMEM and are added, times their scale, into fp32 registers.
+//
+// Scales and bias are read by plain loads: the kernel may run beside the previous one of its stream,
+// which may be writing them until pdl_wait, and ld.global.nc is only for memory that stays constant.
 #pragma once
 #include "opq_device.cuh"
 #include "opq_fp8_format.cuh"
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
                 const int idx = u * EPT + et, b = c + idx / BX, m = m0 + idx % BX;
                 pre[u] = 0.0f;
                 if (b < b1 && m < A.M)
-                    pre[u] = __ldg(A.xs + (int64_t)b * A.ld_xs + m) * __ldg(A.ws + (int64_t)b * A.ld_ws + n_blk);
+                    pre[u] = A.xs[(int64_t)b * A.ld_xs + m] * A.ws[(int64_t)b * A.ld_ws + n_blk];
             }
         };
         fetch(b0);
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
         }
         const int rows = A.M - m0 < BX ? A.M - m0 : BX;
         if (S == 1) {
-            const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(__ldg(A.bias + n)) : 0.0f;
+            const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(A.bias[n]) : 0.0f;
             if (ok && n < A.N) {
 #pragma unroll
                 for (int j = 0; j < C::CW; ++j)
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
             const int e = threadIdx.x & 127;
             const int m0 = m_blk * BX, n = n_blk * 128 + e;
             const int rows = A.M - m0 < BX ? A.M - m0 : BX;
-            const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(__ldg(A.bias + n)) : 0.0f;
+            const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(A.bias[n]) : 0.0f;
             for (int j = rank + S * (threadIdx.x >> 7); j < rows; j += S * (C::THREADS / 128)) {
                 // all ranges' sums asked for at once, added in rank order
                 const uint32_t at = sbase + (uint32_t)(j * 128 + e) * 4u;
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
             const int n0 = n_blk * BN + half * C::HALF;                     // and column
             if (A.bias != nullptr) {
                 __syncwarp();
-                for (int j = lane; j < C::HALF; j += 32) bias_s[j] = n0 + j < A.N ? __ldg(A.bias + n0 + j) : (uint16_t)0;
+                for (int j = lane; j < C::HALF; j += 32) bias_s[j] = n0 + j < A.N ? A.bias[n0 + j] : (uint16_t)0;
                 __syncwarp();      // every lane reads what all lanes stored
             }
             float2 acc[C::HALF / 2];
