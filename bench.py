@@ -26,6 +26,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -52,10 +53,14 @@ def load_peaks():
 
 
 def kernel_source_hash():
+    """Of the kernels' code: comments and the spaces around them are left out."""
     h = hashlib.sha256()
     for rel in KERNEL_SOURCES:
-        with open(os.path.join(ROOT, rel), "rb") as f:
-            h.update(f.read())
+        with open(os.path.join(ROOT, rel), encoding="utf-8") as f:
+            code = re.sub(r"(\"(?:\\.|[^\"\\])*\"|'(?:\\.|[^'\\])*')|//[^\n]*|/\*.*?\*/",
+                          lambda m: m.group(1) or " ", f.read(), flags=re.S)
+        lines = (" ".join(line.split()) for line in code.splitlines())
+        h.update("\n".join(line for line in lines if line).encode() + b"\0")
     return h.hexdigest()[:16]
 
 
