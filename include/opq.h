@@ -362,7 +362,9 @@ opq_status opq_fp8_quantize(const void *x, int32_t dtype, int64_t R, int64_t K, 
  *   x, x_scales      codes [M, ldx] and scales [ceil(K / 128), ld_xs] with block_rows = 1
  *   w, w_scales      codes [N, ldw] and scales [ceil(K / 128), ld_ws] with block_rows = 128
  *   bias             16-bit [N] of type dtype, or NULL for none
- *   activation       OPQ_ACT_*, evaluated as by opq_linear_fused
+ *   activation       OPQ_ACT_*, to fp32's accuracy: a relative error of (32 + 6 |z|) 2^-24 at most before
+ *                    the one rounding, z = v (SiLU) or 2 sqrt(2/pi) (v + 0.044715 v^3) (GELU) of the
+ *                    argument v (opq_linear_fused's hardware tanh may be 2.5e-4 |v| off)
  *   y                16-bit [M, ldy] of type dtype, written; ldy >= N
  * ldx, ldw >= K and multiples of 16; K % 32 == 0. The blocks' sums are formed by the tensor cores
  * (fp32 accumulators), scaled and added in fp32 in a fixed order, and rounded once.
