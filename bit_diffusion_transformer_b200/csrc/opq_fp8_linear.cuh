@@ -550,7 +550,7 @@ struct WideCfg {
 
 struct WideArgs {
     LinearArgs l;
-    int tma_store;      // y rows are 16-byte aligned
+    int tma_store;      // y rows start and end on 16-byte boundaries
 };
 
 template <int CG>
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
                         bulk_commit();
                     }
                 } else {
-                    // rows that TMA cannot address (N % 8 != 0): lanes along the columns, one element
+                    // rows that TMA cannot store (ldy or N % 8 != 0): lanes along the columns, one element
                     // each, no branch per row (4096 x 11521 x 128 44 us against 24 with N = 11520; in
                     // words, with the odd rows' edges apart, 148)
                     __syncwarp();

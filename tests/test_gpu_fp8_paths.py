@@ -46,3 +46,18 @@ def test_bias_of_each_tile_over_one_block(M, N):
     bias = torch.arange(N, device=DEV).remainder(509).sub(254).to(torch.bfloat16)
     for K in (96, 128):
         check(operands(M, N, K, seed=K), bias)
+
+
+@pytest.mark.parametrize("M,K", [(5, 96), (20, 640), (300, 384), (1100, 640), (2001, 640)])
+@pytest.mark.parametrize("N", [3840, 3841, 3845, 3847, 3876])
+@pytest.mark.parametrize("pad", [0, 1, 8, 24])
+def test_nothing_beside_the_output_is_written(M, N, K, pad):
+    """The output inside a wider buffer, its rows aligned to 16 bytes or not, its last column anywhere."""
+    ops = operands(M, N, K, seed=M)
+    bias = normal(N, seed=7)
+    buf = torch.full((M + 16, -(-N // 8) * 8 + pad), 99.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[8:M + 8, :N]
+    opq.fp8_linear(*ops, bias=bias, out=out)
+    assert torch.equal(out, opq.fp8_linear(*ops, bias=bias))
+    out.fill_(99.0)
+    assert bool((buf == 99.0).all())
