@@ -350,11 +350,16 @@ opq_status opq_fp8_linear(const uint8_t *x, int64_t ldx, const float *x_scales, 
     a.ws = w_scales;
     a.bias = static_cast<const uint16_t *>(bias);
     a.y = static_cast<uint16_t *>(y);
+    a.x = x;
+    a.w = w;
+    a.ldx = ldx;
+    a.ldw = ldw;
     a.ld_xs = ld_xs;
     a.ld_ws = ld_ws;
     a.ldy = ldy;
     a.M = (int)M;
     a.N = (int)N;
+    a.K = (int)K;
     a.kblocks = (int)((K + kBlock - 1) / kBlock);
     a.act = activation;
     return dtype == OPQ_DTYPE_BF16 ? run_linear<DT_BF16>(a, x, ldx, w, ldw, K, stream)

@@ -23,8 +23,10 @@ struct LinearArgs {
     const float *ws;        // [kblocks][ld_ws]
     const uint16_t *bias;   // 16-bit [N], or null
     uint16_t *y;            // 16-bit [M, ldy]
+    const uint8_t *x, *w;   // codes, for redo_tile alone (the others come through tensor maps)
+    int64_t ldx, ldw;
     int64_t ld_xs, ld_ws, ldy;
-    int M, N, kblocks;
+    int M, N, K, kblocks;
     int m_tiles, n_tiles;
     int act;
 };
@@ -155,6 +157,119 @@ __device__ __forceinline__ void activate_all(float2 (&v)[N], int act) {
     }
 }
 
+// A block's sums are scaled by one number, s = sx sw, in the fused multiply-add that adds them up. The
+// scales are any fp32 numbers, so s may overflow (and make a sum of zero a NaN) or fall below the
+// normal range (and lose bits) where the scaled sums do neither. Such sums (0, or 2^-18 to 2^25) are
+// multiplied by one scale, then added times the other: the smaller first where the product is large,
+// the larger first where it is small, so that the normal range is left only if the result leaves it.
+//
+// The loops that add the blocks up cannot ask for it: a choice inside them, or a second such loop beside
+// them, cost 4 to 20% of the product (registers). They keep the smallest and the largest product they
+// met. A CTA whose sums can have lost by them (lost_by_scales) goes over its tiles again on mma.sync,
+// straight from global memory and many times slower. No scales of real data come to that, and the
+// asking costs them 1% (4096 x 10240 x 3840 138.0 -> 139.6 us, 256 x 3840 x 3840 12.95 -> 13.35; with every
+// tile done again 13 and 1 ms).
+constexpr float kNormal = 1.1754943508222875e-38f, kLargest = 3.4028234663852886e38f;
+__device__ __forceinline__ bool two_factors(float sx, float sw) {
+    const float s = fabsf(sx * sw);
+    return !(s >= kNormal && s <= kLargest) && sx != 0.0f && sw != 0.0f;
+}
+// Products below the normal range are off by up to 2^-150, so each block's part of a sum by up to
+// 2^-125: that shows in sums below 2^-100. Sums of zero stay (zero rows against zero blocks of W).
+template <int N>
+__device__ __forceinline__ bool small_sums(const float2 (&v)[N]) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float x = fabsf(v[j].x), y = fabsf(v[j].y);
+        any = any || (x < 7.888609052210118e-31f && x > 0.0f) || (y < 7.888609052210118e-31f && y > 0.0f);
+    }
+    return any;
+}
+template <int N>
+__device__ __forceinline__ bool lost_by_scales(float smallest, float largest, const float2 (&v)[N]) {
+    if (smallest >= kNormal && largest <= kLargest) return false;
+    return smallest == 0.0f || largest > kLargest || small_sums(v);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ uint32_t decode_f16x2(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return h;
+}
+
+// Rows m0 .. m0 + 16 MT - 1, features n0 .. n0 + cols - 1 (past the ends too) once more by `warps` warps (a
+// multiple of MT), this one the `warp`-th, where a block has a scale in two factors. The k order inside a
+// 128-column block is free as long as both operands have it: a lane takes eight codes of each row at a
+// time, two MMAs' worth. e4m3 is exact in fp16, and the products in fp32.
+template <int DT, int MT>
+__device__ __forceinline__ void redo_tile(const LinearArgs &A, int m0, int n0, int cols, int warp, int warps) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int mb = m0 + warp % MT * 16;
+    if (mb >= A.M) return;
+    bool two = false;
+    const float *sx = A.xs + (mb + (lane & 15) < A.M ? mb + (lane & 15) : mb);
+    for (int nb = n0; nb < n0 + cols && nb < A.N; nb += kBlock) {
+        const float *sw = A.ws + nb / kBlock;
+#pragma unroll 8
+        for (int b = lane >> 4; b < A.kblocks; b += 2) two |= two_factors(sx[(int64_t)b * A.ld_xs], sw[(int64_t)b * A.ld_ws]);
+    }
+    if (!__any_sync(0xFFFFFFFFu, two)) return;
+    const int r0 = mb + g < A.M ? mb + g : A.M - 1, r1 = mb + g + 8 < A.M ? mb + g + 8 : A.M - 1;
+    const float *sx0 = A.xs + r0, *sx1 = A.xs + r1;
+#pragma unroll 1
+    for (int nb = n0 + warp / MT * 8; nb < n0 + cols && nb < A.N; nb += warps / MT * 8) {
+        const int n = nb + g < A.N ? nb + g : A.N - 1;
+        const float *sw = A.ws + nb / kBlock;
+        const uint8_t *x0 = A.x + (int64_t)r0 * A.ldx + t * 8, *x1 = A.x + (int64_t)r1 * A.ldx + t * 8;
+        const uint8_t *w0 = A.w + (int64_t)n * A.ldw + t * 8;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int b = 0; b < A.kblocks; ++b) {
+            float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const int end = (b + 1) * kBlock < A.K ? (b + 1) * kBlock : A.K;
+#pragma unroll 1
+            for (int k = b * kBlock; k < end; k += 32) {
+                const uint2 xa = *reinterpret_cast<const uint2 *>(x0 + k), xb = *reinterpret_cast<const uint2 *>(x1 + k);
+                const uint2 wv = *reinterpret_cast<const uint2 *>(w0 + k);
+                const uint32_t a0[4] = {decode_f16x2(xa.x), decode_f16x2(xb.x), decode_f16x2(xa.x >> 16), decode_f16x2(xb.x >> 16)};
+                const uint32_t b0[2] = {decode_f16x2(wv.x), decode_f16x2(wv.x >> 16)};
+                mma_f16(p, a0, b0);
+                const uint32_t a1[4] = {decode_f16x2(xa.y), decode_f16x2(xb.y), decode_f16x2(xa.y >> 16), decode_f16x2(xb.y >> 16)};
+                const uint32_t b1[2] = {decode_f16x2(wv.y), decode_f16x2(wv.y >> 16)};
+                mma_f16(p, a1, b1);
+            }
+            const float w = sw[(int64_t)b * A.ld_ws];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = (i ? sx1 : sx0)[(int64_t)b * A.ld_xs];
+                float first = 1.0f, second = x * w;
+                if (two_factors(x, w)) {
+                    const bool x_first = (fabsf(x) > fabsf(w)) != (fabsf(second) > 1.0f);
+                    first = x_first ? x : w;
+                    second = x_first ? w : x;
+                }
+                sum[2 * i] = fmaf(p[2 * i] * first, second, sum[2 * i]);
+                sum[2 * i + 1] = fmaf(p[2 * i + 1] * first, second, sum[2 * i + 1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = mb + g + (i / 2) * 8, c = nb + 2 * t + (i & 1);
+            if (m < A.M && c < A.N) {
+                const float bv = A.bias != nullptr ? unpack16_1<DT>(A.bias[c]) : 0.0f;
+                A.y[(int64_t)m * A.ldy + c] = pack16_1<DT>(activate(sum[i] + bv, A.act));
+            }
+        }
+    }
+}
+
 // mbar_wait with the clock left alone at first: reading the time and the limit costs several
 // hundred cycles, as much as a block's MMAs, and a wait here rarely succeeds at its first try but
 // nearly always within a few. Only a wait that outlasts kSpins tries comes to the time limit.
@@ -239,6 +354,17 @@ __device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int32_t c0, in
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// the same, and whether any of the threads came with `on`
+__device__ __forceinline__ bool named_bar_any(int id, int threads, bool on) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any) : "r"(id), "r"(threads), "r"((int)on) : "memory");
+    return any != 0;
+}
 
 // ---------------------------------------------------------------------------------------------
 // Narrow tiles: 128 rows of W (the MMA's M, so that a TMEM lane is an output feature) x BX rows
@@ -301,9 +427,11 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
     uint64_t *acc_empty = done + C::STAGES;
     uint64_t *drain = acc_empty + C::NACC;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
+    volatile uint32_t *low_slot = tmem_slot + 1;     // a scale product lies outside the normal range
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+        *low_slot = 0;
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&done[s], 1);
@@ -331,6 +459,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
 
     const int S = (int)cluster_size(), rank = (int)cluster_rank();
     const int tile = (int)(blockIdx.x / (unsigned)S);
+    bool redo = false;      // this thread saw sums that lost by their scales
     const int n_blk = tile / A.m_tiles, m_blk = tile - n_blk * A.m_tiles;
     const int b0 = (int)((int64_t)A.kblocks * rank / S), b1 = (int)((int64_t)A.kblocks * (rank + 1) / S);
 
@@ -399,8 +528,14 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
             for (int u = 0; u < PER; ++u) {
                 const int idx = u * EPT + et, b = c + idx / BX, m = m0 + idx % BX;
                 pre[u] = 0.0f;
-                if (b < b1 && m < A.M)
-                    pre[u] = A.xs[(int64_t)b * A.ld_xs + m] * A.ws[(int64_t)b * A.ld_ws + n_blk];
+                if (b < b1 && m < A.M) {
+                    const float sx = A.xs[(int64_t)b * A.ld_xs + m], sw = A.ws[(int64_t)b * A.ld_ws + n_blk];
+                    pre[u] = sx * sw;
+                    if (two_factors(sx, sw)) {
+                        *low_slot = 1;
+                        redo = redo || pre[u] == 0.0f || fabsf(pre[u]) > 1.0f;
+                    }
+                }
             }
         };
         fetch(b0);
@@ -438,6 +573,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
                 }
             }
         }
+        if (*low_slot != 0) redo = redo || small_sums(acc);     // (set before the last chunk's barrier)
         const int rows = A.M - m0 < BX ? A.M - m0 : BX;
         if (S == 1) {
             const float bv = (A.bias != nullptr && n < A.N) ? unpack16_1<DT>(A.bias[n]) : 0.0f;
@@ -462,7 +598,7 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
 
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    redo = __syncthreads_or(redo) != 0;
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
     if (S > 1) {
         __syncwarp();
@@ -490,6 +626,8 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
         cluster_arrive();   // no CTA leaves while another still reads its sums
         cluster_wait();
     }
+    // (behind the cluster's stores of the same rows)
+    if (redo) redo_tile<DT, BX / 16>(A, m_blk * BX, n_blk * 128, 128, warp, C::THREADS / 32);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -824,6 +962,8 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
         int ob = 0;
         bool ready = false;      // the next block's sums are known to be complete, and `s` is its scale
         float s = 0.0f;
+        float smallest = 1.0f, largest = 1.0f;     // scale products
+        bool redo = false;
         pdl_wait();
         for (int t = first; t < tiles && ok; t += step) {
             const int n_blk = t / A.m_tiles, m_blk = t - n_blk * A.m_tiles;
@@ -843,6 +983,8 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
                     if (!(ok = warp_wait8(&done[sd], sph))) break;
                     s = lds_f32(my_scale + slot) * lds_f32(w_scale + slot);
                 }
+                smallest = fminf(smallest, fabsf(s));
+                largest = fmaxf(largest, fabsf(s));
                 tc_fence_after();
                 if (++sd == C::STAGES) { sd = 0; sph ^= 1u; }
                 slot = slot == (C::RING - 1) * C::SCALE_WORDS * 4 ? 0 : slot + C::SCALE_WORDS * 4;
@@ -878,6 +1020,7 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
                 if (++a == C::NACC) a = 0;
             }
             if (!ok) break;
+            redo = redo || lost_by_scales(smallest, largest, acc);
             // The rows' outputs, 32 columns at a time: each lane leaves its row's 64 bytes in shared
             // memory in the TMA store's swizzle. The store is asynchronous because all CTAs finish
             // their tiles together: 10 MB at once, 2 us of L2 writes (stored by the warps
@@ -932,6 +1075,12 @@ __global__ void __launch_bounds__(WideCfg<CG, BN>::THREADS, 1)
             }
         }
         bulk_wait_all();
+        __syncwarp();
+        if (named_bar_any(1, 256, redo))      // (the rows are stored: all warps come here behind their stores)
+            for (int t = first; t < tiles && ok; t += step) {
+                const int n_blk = t / A.m_tiles, m_blk = t - n_blk * A.m_tiles;
+                redo_tile<DT, 8>(A, m_blk * 128 * CG + (int)rank * 128, n_blk * BN, BN, warp - 4, 8);
+            }
     }
 
     __syncwarp();
