@@ -3,6 +3,7 @@ binding of its 8-bit calls, in-tree."""
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -27,6 +28,16 @@ def _nvcc() -> str:
     return "nvcc"
 
 
+def _cuda_include() -> str:
+    """The CUDA headers beside the nvcc in use (which may be a name on PATH, or a link into the toolkit)."""
+    nvcc = shutil.which(_nvcc()) or _nvcc()
+    for path in (nvcc, os.path.realpath(nvcc)):
+        include = os.path.join(os.path.dirname(os.path.dirname(path)), "include")
+        if os.path.exists(os.path.join(include, "cuda_runtime_api.h")):
+            return include
+    raise FileNotFoundError(f"no CUDA headers beside {nvcc}")
+
+
 def _older(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -47,11 +58,10 @@ def _start_ext(obj: str) -> subprocess.Popen:
     """Compile the torch binding (host code only)."""
     import torch
     tinc = os.path.join(os.path.dirname(torch.__file__), "include")
-    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     return subprocess.Popen(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE,
                              "-isystem", tinc, "-isystem", os.path.join(tinc, "torch", "csrc", "api", "include"),
-                             "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+                             "-isystem", sysconfig.get_paths()["include"], "-isystem", _cuda_include(),
                              "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj])
 
 
@@ -76,14 +86,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
     try:
         jobs = [subprocess.Popen([_nvcc(), *flags, "-c", os.path.join(CSRC, src), "-o", obj])
                 for src, obj in zip(SOURCES, objs)]
+        ext_job = ext_error = None
         if ext:
-            jobs.append(_start_ext(ext_obj))
+            try:
+                ext_job = _start_ext(ext_obj)
+            except (ImportError, OSError) as e:
+                ext_error = e
         codes = [j.wait() for j in jobs]
+        ext_code = ext_job.wait() if ext_job else 0
+        # the library first: it does not need the binding
         if any(codes):
-            raise subprocess.CalledProcessError(next(c for c in codes if c), "compiler")
+            raise subprocess.CalledProcessError(next(c for c in codes if c), "nvcc")
         if lib:
             subprocess.check_call([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs])
             os.replace(tmp, SO)
+        if ext_error:
+            raise ext_error
+        if ext_code:
+            raise subprocess.CalledProcessError(ext_code, f"g++ {EXT_SOURCE}")
         if ext:
             _link_ext(ext_obj, tmp)
             os.replace(tmp, EXT)
