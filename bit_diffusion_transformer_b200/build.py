@@ -50,7 +50,19 @@ def _stale() -> bool:
     return _older(SO, deps)
 
 
+def _torch_version() -> str:
+    import torch
+    return torch.__version__
+
+
 def _ext_stale() -> bool:
+    """Older than its sources, or built for another torch (whose C++ interface need not be the same)."""
+    try:
+        with open(EXT + ".torch") as f:
+            if f.read() != _torch_version():
+                return True
+    except (OSError, ImportError):      # (no torch: building the binding says so)
+        return True
     return _older(EXT, [os.path.join(CSRC, EXT_SOURCE), os.path.join(INCLUDE, "opq.h")])
 
 
@@ -107,6 +119,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if ext:
             _link_ext(ext_obj, tmp)
             os.replace(tmp, EXT)
+            with open(EXT + ".torch", "w") as f:
+                f.write(_torch_version())
     finally:
         for f in objs + [ext_obj, tmp]:
             if os.path.exists(f):

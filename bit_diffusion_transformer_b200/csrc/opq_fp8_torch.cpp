@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <stdexcept>
 #include <string>
@@ -377,4 +378,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fp8", nullptr, -1, g_methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fp8(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__fp8(void) {
+    PyObject *m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "TORCH_VERSION", TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -84,3 +84,31 @@ def test_a_failed_kernel_file_leaves_the_old_library(tree, monkeypatch):
     with pytest.raises(subprocess.CalledProcessError):
         b.build()
     assert (tree / "libopq.so").read_text() == "old" and sorted(os.listdir(tree)) == ["libopq.so"]
+
+
+def test_binding_is_built_again_for_another_torch(tree, monkeypatch):
+    jobs = Jobs(monkeypatch)
+    b.build()
+    n = len(jobs.commands)
+    b.build()
+    assert len(jobs.commands) == n             # nothing to do
+    import torch
+    monkeypatch.setattr(torch, "__version__", "99.1.0+cu999")
+    b.build()
+    again = jobs.commands[n:]
+    assert again and all("nvcc" not in c[0] for c in again)     # the binding alone
+    b.build()
+    assert len(jobs.commands) == n + len(again)
+
+
+def test_binding_of_another_torch_is_refused(monkeypatch):
+    import torch
+
+    from bit_diffusion_transformer_b200 import build, fp8
+    build.build()
+    monkeypatch.setattr(fp8, "_ext", None)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "99.1.0+cu999")
+        with pytest.raises(ImportError, match="99.1.0"):
+            fp8._load()
+    assert fp8._load() is not None
