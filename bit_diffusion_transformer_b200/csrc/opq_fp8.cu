@@ -3,8 +3,11 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "opq.h"
 #include "opq_fp8_cache.cuh"
@@ -230,6 +233,28 @@ opq_status check_side(const opq_fp8_cache &c, const opq_rows &r, int64_t heads) 
     return OPQ_OK;
 }
 
+// Whether elements written through these strides can share memory: `inner` contiguous ones at every
+// combination of the dimensions' offsets. Each dimension, in the order of their strides, must step
+// past all that the smaller ones span (a layout that interleaves them otherwise is refused too).
+bool overlapping(int64_t inner, std::initializer_list<std::pair<int64_t, int64_t>> size_stride) {
+    std::pair<int64_t, int64_t> d[3];
+    int n = 0;
+    for (const auto &s : size_stride)
+        if (s.first > 1) d[n++] = {s.second, s.first - 1};
+    std::sort(d, d + n);
+    __int128 span = inner;      // elements from the first to behind the last
+    for (int i = 0; i < n; ++i) {
+        if (d[i].first < span) return true;
+        span += (__int128)d[i].first * d[i].second;
+    }
+    return false;
+}
+bool overlapping(const opq_fp8_cache &c, int64_t pages, int64_t page_size, int64_t heads) {
+    return overlapping(c.head_dim, {{pages, c.page_stride}, {page_size, c.token_stride}, {heads, c.head_stride}}) ||
+           overlapping((c.head_dim + kBlock - 1) / kBlock,
+                       {{pages, c.scale_page_stride}, {page_size, c.scale_token_stride}, {heads, c.scale_head_stride}});
+}
+
 CacheSide make_side(const opq_fp8_cache &c, const opq_rows &r) {
     CacheSide s{};
     s.codes = c.codes;
@@ -248,9 +273,10 @@ CacheSide make_side(const opq_fp8_cache &c, const opq_rows &r) {
     return s;
 }
 
-// what the two cache calls check alike, before any pointer is looked at by the driver
+// What the two cache calls check alike, before any pointer is looked at by the driver. out_rows: the
+// rows that a read writes; below zero, the cache itself is written.
 opq_status check_cache(const opq_fp8_cache *cache, const opq_rows *rows, int32_t tensors, int64_t pages,
-                       int64_t page_size, int64_t heads, int32_t dtype) {
+                       int64_t page_size, int64_t heads, int32_t dtype, int64_t out_rows) {
     if (!cache || !rows || tensors < 1 || tensors > 2 || pages < 1 || page_size < 1 || heads < 1 || !dtype_ok(dtype))
         return OPQ_ERR_INVALID_ARG;
     if (pages > INT32_MAX || page_size > INT32_MAX || heads > INT32_MAX) return OPQ_ERR_UNSUPPORTED_SHAPE;
@@ -260,6 +286,10 @@ opq_status check_cache(const opq_fp8_cache *cache, const opq_rows *rows, int32_t
     }
     for (int i = 0; i < tensors; ++i)
         if (!cache[i].scales || !cache[i].codes || !rows[i].data) return OPQ_ERR_INVALID_ARG;
+    for (int i = 0; i < tensors; ++i)
+        if (out_rows < 0 ? overlapping(cache[i], pages, page_size, heads)
+                         : overlapping(cache[i].head_dim, {{out_rows, rows[i].token_stride}, {heads, rows[i].head_stride}}))
+            return OPQ_ERR_INVALID_ARG;
     for (int i = 0; i < tensors; ++i)
         if (!aligned4(cache[i].scales)) return OPQ_ERR_MISALIGNED;
     for (int i = 0; i < tensors; ++i) {
@@ -373,7 +403,7 @@ opq_status opq_fp8_cache_write(const opq_fp8_cache *cache, const opq_rows *rows,
     if (tokens == 0) return OPQ_OK;
     if (!slots) return OPQ_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return OPQ_ERR_MISALIGNED;
-    opq_status s = check_cache(cache, rows, tensors, pages, page_size, heads, dtype);
+    opq_status s = check_cache(cache, rows, tensors, pages, page_size, heads, dtype, -1);
     if (s == OPQ_OK) s = check_device({slots});
     if (s != OPQ_OK) return s;
     WriteArgs a{};
@@ -408,7 +438,7 @@ opq_status opq_fp8_cache_read(const opq_fp8_cache *cache, const opq_rows *rows, 
     if (seqs > INT32_MAX - 1 || row_count > INT32_MAX) return OPQ_ERR_UNSUPPORTED_SHAPE;
     if (!cu_rows || !page_table || table_width < 1 || ld_table < table_width) return OPQ_ERR_INVALID_ARG;
     if (!aligned4(cu_rows) || !aligned4(page_table) || !aligned4(starts)) return OPQ_ERR_MISALIGNED;
-    opq_status s = check_cache(cache, rows, tensors, pages, page_size, heads, dtype);
+    opq_status s = check_cache(cache, rows, tensors, pages, page_size, heads, dtype, row_count);
     if (s == OPQ_OK) s = check_device({cu_rows, page_table});
     if (s == OPQ_OK && starts) s = check_device({starts});
     if (s != OPQ_OK) return s;

@@ -381,7 +381,9 @@ opq_status opq_fp8_linear(const uint8_t *x, int64_t ldx, const float *x_scales, 
  *     scales + page * scale_page_stride + slot * scale_token_stride
  *            + head * scale_head_stride + c / 128                                        (floats)
  * so any order of the page's tokens and heads is served. Code strides are multiples of 16,
- * head_dim is a multiple of 16; elements must not overlap.
+ * head_dim is a multiple of 16. Elements of a cache that is written, and of rows that are, may not
+ * overlap: in the order of the strides, each dimension steps past all that the smaller ones span
+ * (INVALID_ARG otherwise). Inputs may be broadcast.
  */
 typedef struct opq_fp8_cache {
     uint8_t *codes;
