@@ -33,7 +33,7 @@ EXPORTS = ["opq_quantize", "opq_dequantize", "opq_linear_workspace_size", "opq_l
            "opq_linear_grouped_fused", "opq_alpha_search", "opq_alpha_search_workspace_size",
            "opq_quantize_bits", "opq_dequantize_bits", "opq_set_wait_limit_ns",
            "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size", "opq_dequantize_batched",
-           "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_cache_write", "opq_fp8_cache_read"]
+           "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_linear_plan", "opq_fp8_cache_write", "opq_fp8_cache_read"]
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2}
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -82,6 +82,7 @@ def load(path: str = LIB_PATH):
     lib.opq_linear_bits_workspace_size.argtypes = [I, I, I, ctypes.c_int32, ctypes.POINTER(S)]
     lib.opq_fp8_quantize.argtypes = [P, ctypes.c_int32, I, I, I, I, P, I, P, I, P]
     lib.opq_fp8_linear.argtypes = [P, I, P, I, I, I, P, I, P, I, I, P, ctypes.c_int32, P, ctypes.c_int32, I, P]
+    lib.opq_fp8_linear_plan.argtypes = [I, I, I] + [ctypes.POINTER(ctypes.c_int)] * 3
     lib.opq_fp8_cache_write.argtypes = [P, P, ctypes.c_int32, I, I, I, ctypes.c_int32, I, P, P]
     lib.opq_fp8_cache_read.argtypes = [P, P, ctypes.c_int32, I, I, I, ctypes.c_int32, I, P, I, P, I, I, P, P]
     lib.opq_status_string.argtypes = [ctypes.c_int]
@@ -91,8 +92,8 @@ def load(path: str = LIB_PATH):
               "opq_linear_grouped_workspace_size", "opq_linear_fused", "opq_linear_grouped_fused",
               "opq_alpha_search", "opq_alpha_search_workspace_size", "opq_quantize_bits", "opq_dequantize_bits",
               "opq_set_wait_limit_ns", "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size",
-              "opq_dequantize_batched", "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_cache_write",
-              "opq_fp8_cache_read"):
+              "opq_dequantize_batched", "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_linear_plan",
+              "opq_fp8_cache_write", "opq_fp8_cache_read"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -455,4 +456,4 @@ def set_wait_limit_ns(ns: int = 0):
     _check(load().opq_set_wait_limit_ns(int(ns)), "opq_set_wait_limit_ns")
 
 
-from .fp8 import fp8_cache_read, fp8_cache_write, fp8_linear, fp8_quantize  # noqa: E402
+from .fp8 import fp8_cache_read, fp8_cache_write, fp8_linear, fp8_linear_plan, fp8_quantize  # noqa: E402

@@ -199,6 +199,10 @@ Fp8Plan make_fp8_plan(int64_t M, int64_t N, int64_t K) {
     return p;
 }
 
+bool product_sizes_ok(int64_t M, int64_t N, int64_t K) {
+    return K % 32 == 0 && K <= INT32_MAX - 128 && M <= INT32_MAX - 256 && N <= INT32_MAX - 256;
+}
+
 template <int DT>
 opq_status run_linear(LinearArgs a, const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t K, void *stream) {
     const Fp8Plan p = make_fp8_plan(a.M, a.N, K);
@@ -365,8 +369,7 @@ opq_status opq_fp8_linear(const uint8_t *x, int64_t ldx, const float *x_scales, 
     if (M < 1 || N < 1 || K < 1 || !dtype_ok(dtype)) return OPQ_ERR_INVALID_ARG;
     if (activation != OPQ_ACT_NONE && activation != OPQ_ACT_SILU && activation != OPQ_ACT_GELU_TANH)
         return OPQ_ERR_INVALID_ARG;
-    if (K % 32 != 0 || K > INT32_MAX - 128 || M > INT32_MAX - 256 || N > INT32_MAX - 256)
-        return OPQ_ERR_UNSUPPORTED_SHAPE;
+    if (!product_sizes_ok(M, N, K)) return OPQ_ERR_UNSUPPORTED_SHAPE;
     if (ldx < K || ldx % 16 != 0 || ldw < K || ldw % 16 != 0 || ldy < N || ld_xs < M || ld_ws < (N + 127) / 128)
         return OPQ_ERR_INVALID_ARG;
     if (!x_scales || !w_scales) return OPQ_ERR_INVALID_ARG;
@@ -394,6 +397,16 @@ opq_status opq_fp8_linear(const uint8_t *x, int64_t ldx, const float *x_scales, 
     a.act = activation;
     return dtype == OPQ_DTYPE_BF16 ? run_linear<DT_BF16>(a, x, ldx, w, ldw, K, stream)
                                    : run_linear<DT_FP16>(a, x, ldx, w, ldw, K, stream);
+}
+
+opq_status opq_fp8_linear_plan(int64_t M, int64_t N, int64_t K, int *rows, int *cols, int *ctas) {
+    if (M < 1 || N < 1 || K < 1) return OPQ_ERR_INVALID_ARG;
+    if (!product_sizes_ok(M, N, K)) return OPQ_ERR_UNSUPPORTED_SHAPE;
+    const Fp8Plan p = make_fp8_plan(M, N, K);
+    if (rows) *rows = p.bn ? 128 * p.cg : p.bx;
+    if (cols) *cols = p.bn ? p.bn : 128;
+    if (ctas) *ctas = p.bn ? p.cg : p.split;
+    return OPQ_OK;
 }
 
 opq_status opq_fp8_cache_write(const opq_fp8_cache *cache, const opq_rows *rows, int32_t tensors, int64_t pages,

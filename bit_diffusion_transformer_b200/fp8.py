@@ -69,6 +69,13 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     return (_ext or _load()).linear(x, x_scales, w, w_scales, bias, code, dtype, out)
 
 
+def fp8_linear_plan(M: int, N: int, K: int):
+    """The tiles fp8_linear uses for x [M, K] and W [N, K] -> (rows of x, rows of W, CTAs that share a tile)."""
+    out = [ctypes.c_int() for _ in range(3)]
+    _opq._check(_opq.load().opq_fp8_linear_plan(M, N, K, *[ctypes.byref(v) for v in out]), "opq_fp8_linear_plan")
+    return tuple(v.value for v in out)
+
+
 class Fp8Cache(ctypes.Structure):
     """Keys or values of a cache (the C struct opq_fp8_cache)."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("head_dim", ctypes.c_int64),

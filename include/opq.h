@@ -374,6 +374,14 @@ opq_status opq_fp8_linear(const uint8_t *x, int64_t ldx, const float *x_scales, 
                           const void *bias, int32_t activation, void *y, int32_t dtype, int64_t ldy, void *stream);
 
 /*
+ * opq_fp8_linear_plan — the tiles opq_fp8_linear uses for this shape (it depends on the shape alone):
+ *   rows, cols  rows of x and of w per tile
+ *   ctas        CTAs that share a tile: a cluster's ranges of blocks (rows <= 64), or a pair (256 x 256)
+ * NULL outputs are left out.
+ */
+opq_status opq_fp8_linear_plan(int64_t M, int64_t N, int64_t K, int *rows, int *cols, int *ctas);
+
+/*
  * A paged cache of keys or of values in the 8-bit block format: `pages` pages of `page_size`
  * token slots, `heads` heads of head_dim channels each, blocks of 128 along a head's channels.
  * The code of (page, slot, head, channel c) is at

@@ -6,6 +6,8 @@ import torch
 
 import bit_diffusion_transformer_b200 as opq
 import fp8_reference as ref
+from fp8_schedules import SCHEDULES
+from test_gpu_fp8_activations import exact, tolerance
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -61,3 +63,23 @@ def test_nothing_beside_the_output_is_written(M, N, K, pad):
     assert torch.equal(out, opq.fp8_linear(*ops, bias=bias))
     out.fill_(99.0)
     assert bool((buf == 99.0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,N,K", list(SCHEDULES))
+def test_every_schedule(M, N, K, act, dtype):
+    """With a bias that differs from column to column, an activation and both types."""
+    ops = operands(M, N, K, seed=N)
+    bias = normal(N, seed=3, dtype=dtype)
+    y = opq.fp8_linear(*ops, bias=bias, act=act, dtype=dtype)
+    _, B, v = ref.linear(*ops, bias)
+    dv = (128 * 2.0 ** -23 + (-(-K // 128) + 2) * 2.0 ** -24) * B + 2.0 ** -24 * (v.abs() + bias.double().abs())
+    if act == "none":
+        fi = torch.finfo(dtype)
+        want, tol = v, dv + (v.abs() + dv) * (fi.eps / 2) + fi.smallest_normal * fi.eps / 2
+    else:
+        want, z, slope = exact(v, act)
+        tol = tolerance(want, z, slope, v, dv, dtype)
+    err = (y.double() - want).abs()
+    assert y.dtype == dtype and bool((err <= tol).all()), f"{int((~(err <= tol)).sum())} of {err.numel()} out"
