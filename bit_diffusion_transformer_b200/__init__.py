@@ -31,7 +31,7 @@ EXPORTS = ["opq_quantize", "opq_dequantize", "opq_linear_workspace_size", "opq_l
            "opq_abi_version", "opq_quantize_grouped", "opq_dequantize_grouped",
            "opq_linear_grouped", "opq_linear_grouped_workspace_size", "opq_linear_fused",
            "opq_linear_grouped_fused", "opq_alpha_search", "opq_alpha_search_workspace_size",
-           "opq_quantize_bits", "opq_dequantize_bits", "opq_set_wait_limit_ns",
+           "opq_quantize_bits", "opq_dequantize_bits", "opq_set_wait_limit_ns", "opq_get_wait_limit_ns",
            "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size", "opq_dequantize_batched",
            "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_linear_plan", "opq_fp8_cache_write", "opq_fp8_cache_read"]
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2}
@@ -76,6 +76,7 @@ def load(path: str = LIB_PATH):
     lib.opq_linear_fused.argtypes = [P, I, I, P, P, P, I, F, P, ctypes.c_int, P, P, S, P]
     lib.opq_linear_grouped_fused.argtypes = [P, I, I, P, P, P, I, I, F, P, ctypes.c_int, P, P, S, P]
     lib.opq_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
+    lib.opq_get_wait_limit_ns.argtypes = [ctypes.POINTER(ctypes.c_uint64)] * 2
     lib.opq_quantize_batched.argtypes = [P, I, F, P]
     lib.opq_dequantize_batched.argtypes = [P, I, F, P]
     lib.opq_linear_bits.argtypes = [P, I, I, P, P, P, I, ctypes.c_int32, F, P, P, S, P]
@@ -91,7 +92,7 @@ def load(path: str = LIB_PATH):
               "opq_linear_noalloc", "opq_device_error", "opq_quantize_grouped", "opq_dequantize_grouped", "opq_linear_grouped",
               "opq_linear_grouped_workspace_size", "opq_linear_fused", "opq_linear_grouped_fused",
               "opq_alpha_search", "opq_alpha_search_workspace_size", "opq_quantize_bits", "opq_dequantize_bits",
-              "opq_set_wait_limit_ns", "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size",
+              "opq_set_wait_limit_ns", "opq_get_wait_limit_ns", "opq_quantize_batched", "opq_linear_bits", "opq_linear_bits_workspace_size",
               "opq_dequantize_batched", "opq_fp8_quantize", "opq_fp8_linear", "opq_fp8_linear_plan",
               "opq_fp8_cache_write", "opq_fp8_cache_read"):
         getattr(lib, f).restype = ctypes.c_int
@@ -454,6 +455,13 @@ def device_error(device=None) -> int:
 def set_wait_limit_ns(ns: int = 0):
     """Time after which the kernels' bounded waits give up on the current device (0: the 4 s default)."""
     _check(load().opq_set_wait_limit_ns(int(ns)), "opq_set_wait_limit_ns")
+
+
+def wait_limit_ns():
+    """The limits in force on the current device, read back from it: (of the OPQ kernels, of the 8-bit ones)."""
+    a, b = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check(load().opq_get_wait_limit_ns(ctypes.byref(a), ctypes.byref(b)), "opq_get_wait_limit_ns")
+    return int(a.value), int(b.value)
 
 
 from .fp8 import fp8_cache_read, fp8_cache_write, fp8_linear, fp8_linear_plan, fp8_quantize  # noqa: E402

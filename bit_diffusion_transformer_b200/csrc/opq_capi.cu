@@ -1121,6 +1121,13 @@ extern "C" opq_status opq_set_wait_limit_ns(uint64_t ns) {
     return e == cudaSuccess ? OPQ_OK : cuda_fail(e);
 }
 
+extern "C" opq_status opq_get_wait_limit_ns(uint64_t *ns, uint64_t *ns_fp8) {
+    cudaError_t e = cudaSuccess;
+    if (ns) e = cudaMemcpyFromSymbol(ns, opqdev::g_wait_limit_ns, sizeof *ns);
+    if (e == cudaSuccess && ns_fp8) e = opqhost::fp8_get_wait_limit(ns_fp8);
+    return e == cudaSuccess ? OPQ_OK : cuda_fail(e);
+}
+
 extern "C" opq_status opq_linear_noalloc(const uint16_t *x, int64_t M, int64_t K, const uint32_t *codes,
                                          const uint32_t *signs, const float *scales, int64_t N, float alpha,
                                          uint16_t *y, void *stream) {

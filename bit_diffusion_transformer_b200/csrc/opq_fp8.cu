@@ -23,6 +23,7 @@ cudaError_t fp8_device_error(uint32_t *err) {
     return e;
 }
 cudaError_t fp8_set_wait_limit(uint64_t ns) { return cudaMemcpyToSymbol(opqdev::g_wait_limit_ns, &ns, sizeof ns); }
+cudaError_t fp8_get_wait_limit(uint64_t *ns) { return cudaMemcpyFromSymbol(ns, opqdev::g_wait_limit_ns, sizeof *ns); }
 }  // namespace opqhost
 
 namespace {

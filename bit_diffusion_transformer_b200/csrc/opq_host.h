@@ -26,8 +26,9 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 OPQ_INTERNAL EncodeTiledFn encode_fn();
 
 // opq_fp8.cu keeps its own copies of the device error word and the wait limit (device symbols
-// belong to their translation unit): read-and-clear, and set
+// belong to their translation unit): read-and-clear, set and read
 OPQ_INTERNAL cudaError_t fp8_device_error(uint32_t *err);
 OPQ_INTERNAL cudaError_t fp8_set_wait_limit(uint64_t ns);
+OPQ_INTERNAL cudaError_t fp8_get_wait_limit(uint64_t *ns);
 
 }  // namespace opqhost

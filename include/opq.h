@@ -468,6 +468,13 @@ opq_status opq_device_error(void *stream, uint32_t *err);
  * call returns; do not change it while library kernels run on other streams.
  */
 opq_status opq_set_wait_limit_ns(uint64_t ns);
+/*
+ * opq_get_wait_limit_ns — the limit in force on the current device, read back from where the kernels
+ * read it: *ns of the OPQ kernels, *ns_fp8 of the 8-bit ones, which keep their own copy (either may be
+ * NULL). The 8-bit product tries a barrier 4096 times before it looks at the clock, so its waits give
+ * up that much later.
+ */
+opq_status opq_get_wait_limit_ns(uint64_t *ns, uint64_t *ns_fp8);
 
 /* Human-readable name of a status. */
 const char *opq_status_string(opq_status s);

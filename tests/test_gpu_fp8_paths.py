@@ -83,3 +83,14 @@ def test_every_schedule(M, N, K, act, dtype):
         tol = tolerance(want, z, slope, v, dv, dtype)
     err = (y.double() - want).abs()
     assert y.dtype == dtype and bool((err <= tol).all()), f"{int((~(err <= tol)).sum())} of {err.numel()} out"
+
+
+def test_the_wait_limit_is_where_the_8_bit_kernels_read_it():
+    assert opq.wait_limit_ns() == (4_000_000_000, 4_000_000_000)
+    try:
+        opq.set_wait_limit_ns(70_000_000)
+        assert opq.wait_limit_ns() == (70_000_000, 70_000_000)
+        check(operands(300, 700, 1024, seed=2))
+    finally:
+        opq.set_wait_limit_ns(0)
+    assert opq.wait_limit_ns() == (4_000_000_000, 4_000_000_000)
