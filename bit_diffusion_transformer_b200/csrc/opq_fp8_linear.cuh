@@ -371,8 +371,9 @@ __device__ __forceinline__ bool named_bar_any(int id, int threads, bool on) {
 // of x. For few rows of x the product is bound by streaming W once; a cluster of S CTAs cuts the
 // tile's blocks into S ranges so that the stream reaches every SM, and the ranges' fp32 sums meet
 // through the cluster's shared memory in rank order (no workspace, the same bits every run).
-// Measured: 1 x 11520 x 3840 10.0 us (44 MB, 0.67 of the copy bandwidth), 32 x 11520 x 3840 12.2,
-// 37 x 3840 x 10240 12.9; one launch costs about 3 us before and after its stream (barriers, the first
+// Measured: 1 x 11520 x 3840 9.9 us (44 MB, 0.68 of the copy bandwidth), 32 x 11520 x 3840 12.0,
+// 37 x 3840 x 10240 12.8 (its 64-row kernel keeps to 80 registers for two CTAs per SM and spills 44
+// bytes); one launch costs about 3 us before and after its stream (barriers, the first
 // copies' latency, the cluster's exchange), and a block is a chain of hand-overs (copy, MMA, sums) of
 // about 0.4 us per CTA, which two CTAs per SM and two issuing warps overlap. Reading W straight into
 // mma.sync operands instead started faster (2.1 us for 512 x 1024 against 2.9) but was bound by its
@@ -386,7 +387,7 @@ struct NarrowCfg {
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int X_BYTES = BX * 128;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = 4;                                   // three CTAs per SM at BX = 16
+    static constexpr int STAGES = 4;                                   // two CTAs per SM (79 to 104 KB each)
     // blocks of W asked for ahead of the previous kernel's end: as many as the first copies take
     // (1 x 3840 x 3840 5.98 -> 5.75 us, 64 x 3840 x 3840 9.67 -> 9.35; ten blocks gain nothing more and
     // cost 37 x 3840 x 10240 1.5 us)
@@ -642,8 +643,10 @@ __global__ void __launch_bounds__(NarrowCfg<BX>::THREADS, 2)
 //                Each block's sums leave TMEM (two accumulators in turn, so the tensor pipe runs
 //                on) and are added times sx[row] sw[block of W]: one scalar per thread and block.
 //                The finished rows go through shared memory and leave by TMA.
-// Measured: 4096 x 10240 x 3840 146 us (2200 TFLOP/s, 0.67 of twice the bf16 rate), with GELU 158;
-// 1089 x 3840 x 3840 19.4 us on single CTAs. A block is 512 cycles of MMA and takes about 850: the
+// Measured: 4096 x 10240 x 3840 140 us (2300 TFLOP/s, 0.70 of twice the bf16 rate; 137 to 146 by box, whose
+// power cap sets the clock), with GELU 160; 1089 x 3840 x 3840 18.3 us on single CTAs. Spills, outside
+// the block loop as far as times show: pairs 12 bytes stored and 32 loaded, 128 x 128 28 and 120,
+// 128 x 256 none. A block is 512 cycles of MMA and takes about 850: the
 // sums of two blocks fill TMEM, so block i + 2 waits for block i's trip through the epilogue (commit to
 // wait 200 cycles, loads 250, hand-back 250), and the epilogue's own work per block is about 560.
 // Leaving out any one of copies, TMEM loads, additions or scales gains 4 to 15%: nothing alone

@@ -50,7 +50,7 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1, out=None):
     """Quantize a 16-bit matrix [R, K] (K % 32 == 0) -> (codes [R, K], scales).
 
     ``block_rows`` 1 gives each row its own scale per 128 columns (activations), 128 gives one
-    scale per 128 x 128 block (weights). Rows may be strided (a multiple of 8 elements).
+    scale per 128 x 128 block (weights). Rows may be strided (a multiple of 8 elements); R is 1 or more.
     ``out`` = (codes, scales) to write into."""
     return (_ext or _load()).quantize(x, block_rows, out)
 
@@ -60,9 +60,9 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     """y = act(x @ W^T + bias) -> [M, N] of ``dtype`` (bfloat16 or float16).
 
     ``x``, ``x_scales`` from fp8_quantize(., 1); ``w``, ``w_scales`` from fp8_quantize(., 128);
-    ``bias`` [N] of the output's type; ``act`` one of ACTIVATIONS. Rows may be strided (codes:
-    multiples of 16), so slices of a batch's codes and scales serve. ``out`` (its type stands for
-    ``dtype``) to write into."""
+    ``bias`` [N] of the output's type; ``act`` one of ACTIVATIONS, evaluated to fp32's accuracy. Rows
+    may be strided (codes: multiples of 16), so slices of a batch's codes and scales serve; M is 1 or
+    more. ``out`` (its type stands for ``dtype``) to write into, inside a wider buffer too."""
     code = _opq.ACTIVATIONS.get(act)
     if code is None:
         raise ValueError(f"opq: act must be one of {', '.join(_opq.ACTIVATIONS)}")
@@ -95,7 +95,7 @@ def fp8_cache_write(k: torch.Tensor, v: torch.Tensor | None, cache, slots: torch
     ``cache`` = (k_codes, k_scales, v_codes, v_scales), or (codes, scales) with ``v`` None: codes
     float8_e4m3fn [pages, page_size, heads, head_dim] and scales float32 [pages, page_size, heads,
     ceil(head_dim / 128)]; views of other layouts (heads before tokens in a page) and slices of a
-    fused projection's output serve. head_dim % 16 == 0; values may have their own head_dim.
+    fused projection's output serve, as long as no two elements share memory. head_dim % 16 == 0; values may have their own head_dim.
     ``slots`` int64 [T]: page * page_size + offset; negative entries are skipped, entries past the
     cache are skipped and reported by device_error() (DEVERR_INDEX). Slots >= 0 must differ."""
     (_ext or _load()).cache_write(k, v, cache, slots)
