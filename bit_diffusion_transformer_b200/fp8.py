@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
 
 import torch
 
@@ -38,7 +39,7 @@ def _load():
             raise ImportError(f"_fp8.so not found at {EXT_PATH}; build it with "
                               f"`python -m bit_diffusion_transformer_b200.build`")
         from . import _fp8
-        if _fp8.TORCH_VERSION != torch.__version__.split("+")[0]:
+        if not re.match(re.escape(_fp8.TORCH_VERSION) + r"(?!\d)", torch.__version__):    # (2.9.0a0+git..: 2.9.0)
             raise ImportError(f"_fp8.so was built for torch {_fp8.TORCH_VERSION}, this is {torch.__version__}; build it "
                               f"again with `python -m bit_diffusion_transformer_b200.build`")
         _fp8.set_error(_opq.OPQError)

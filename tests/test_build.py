@@ -112,3 +112,20 @@ def test_binding_of_another_torch_is_refused(monkeypatch):
         with pytest.raises(ImportError, match="99.1.0"):
             fp8._load()
     assert fp8._load() is not None
+
+
+def test_binding_takes_every_build_of_its_torch(monkeypatch):
+    import torch
+
+    from bit_diffusion_transformer_b200 import build, fp8
+    build.build()
+    number = fp8._load().TORCH_VERSION
+    for version, ok in ((number, True), (number + "+cu130", True), (number + "a0+gitabc.nv25", True),
+                        (number + "7", False), ("1" + number, False)):
+        monkeypatch.setattr(fp8, "_ext", None)
+        monkeypatch.setattr(torch, "__version__", version)
+        if ok:
+            fp8._load()
+        else:
+            with pytest.raises(ImportError):
+                fp8._load()
