@@ -165,14 +165,14 @@ __device__ __forceinline__ void activate_all(float2 (&v)[N], int act) {
 //
 // The loops that add the blocks up cannot ask for it: a choice inside them, or a second such loop beside
 // them, cost 4 to 20% of the product (registers). They keep the smallest and the largest product they
-// met. A CTA whose sums can have lost by them (lost_by_scales) goes over its tiles again on mma.sync,
-// straight from global memory and many times slower. No scales of real data come to that, and the
+// met. A CTA whose sums can have lost by them (lost_by_scales) does the rows in question again on
+// mma.sync, straight from global memory and many times slower. No scales of real data come to that, and the
 // asking costs them 1% (4096 x 10240 x 3840 138.0 -> 139.6 us, 256 x 3840 x 3840 12.95 -> 13.35; with every
-// tile done again 13 and 1 ms).
+// row done again 9 and 0.7 ms).
 constexpr float kNormal = 1.1754943508222875e-38f, kLargest = 3.4028234663852886e38f;
 __device__ __forceinline__ bool two_factors(float sx, float sw) {
     const float s = fabsf(sx * sw);
-    return !(s >= kNormal && s <= kLargest) && sx != 0.0f && sw != 0.0f;
+    return !(s >= kNormal && s <= kLargest) && sx != 0.0f && sw != 0.0f && fabsf(sx) <= kLargest && fabsf(sw) <= kLargest;
 }
 // Products below the normal range are off by up to 2^-150, so each block's part of a sum by up to
 // 2^-125: that shows in sums below 2^-100. Sums of zero stay (zero rows against zero blocks of W).
@@ -205,7 +205,7 @@ __device__ __forceinline__ uint32_t decode_f16x2(uint32_t codes) {
 }
 
 // Rows m0 .. m0 + 16 MT - 1, features n0 .. n0 + cols - 1 (past the ends too) once more by `warps` warps (a
-// multiple of MT), this one the `warp`-th, where a block has a scale in two factors. The k order inside a
+// multiple of MT), this one the `warp`-th: the rows with a scale in two factors. The k order inside a
 // 128-column block is free as long as both operands have it: a lane takes eight codes of each row at a
 // time, two MMAs' worth. e4m3 is exact in fp16, and the products in fp32.
 template <int DT, int MT>
@@ -220,7 +220,9 @@ __device__ __forceinline__ void redo_tile(const LinearArgs &A, int m0, int n0, i
 #pragma unroll 8
         for (int b = lane >> 4; b < A.kblocks; b += 2) two |= two_factors(sx[(int64_t)b * A.ld_xs], sw[(int64_t)b * A.ld_ws]);
     }
-    if (!__any_sync(0xFFFFFFFFu, two)) return;
+    uint32_t rows = __ballot_sync(0xFFFFFFFFu, two);
+    rows = (rows | rows >> 16) & 0xFFFFu;        // the others' bits stay as they are
+    if (rows == 0) return;
     const int r0 = mb + g < A.M ? mb + g : A.M - 1, r1 = mb + g + 8 < A.M ? mb + g + 8 : A.M - 1;
     const float *sx0 = A.xs + r0, *sx1 = A.xs + r1;
 #pragma unroll 1
@@ -234,7 +236,7 @@ __device__ __forceinline__ void redo_tile(const LinearArgs &A, int m0, int n0, i
         for (int b = 0; b < A.kblocks; ++b) {
             float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             const int end = (b + 1) * kBlock < A.K ? (b + 1) * kBlock : A.K;
-#pragma unroll 1
+#pragma unroll 4
             for (int k = b * kBlock; k < end; k += 32) {
                 const uint2 xa = *reinterpret_cast<const uint2 *>(x0 + k), xb = *reinterpret_cast<const uint2 *>(x1 + k);
                 const uint2 wv = *reinterpret_cast<const uint2 *>(w0 + k);
@@ -262,7 +264,7 @@ __device__ __forceinline__ void redo_tile(const LinearArgs &A, int m0, int n0, i
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int m = mb + g + (i / 2) * 8, c = nb + 2 * t + (i & 1);
-            if (m < A.M && c < A.N) {
+            if (m < A.M && c < A.N && (rows >> (g + (i / 2) * 8) & 1)) {
                 const float bv = A.bias != nullptr ? unpack16_1<DT>(A.bias[c]) : 0.0f;
                 A.y[(int64_t)m * A.ldy + c] = pack16_1<DT>(activate(sum[i] + bv, A.act));
             }

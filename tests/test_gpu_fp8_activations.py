@@ -22,6 +22,7 @@ import fp8_reference as ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+F8 = torch.float8_e4m3fn
 DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
 # tile kinds by shape: narrow tiles of 16 rows (one range of blocks, two), of 32, of 64; 128 x 128,
 # 128 x 256 and pairs of 256 x 256 with whole rows and with rows that TMA cannot store
@@ -121,3 +122,23 @@ def test_activation_of_special_values(M, N, K, act, dtype):
     assert bool((y[:, big] == torch.finfo(dt).max).all()) and bool((y[:, low] == 0).all())
     assert bool((y[:, bias == math.inf] == math.inf).all())
     assert bool(torch.isnan(y[:, torch.isnan(bias) | (bias == -math.inf)]).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_nan_and_infinite_sums_stay_where_they_are(M, N, K, act):
+    """Values that share a reciprocal are neighbours along the features or along the rows of x."""
+    g = torch.Generator(DEV).manual_seed(M)
+    xc, xs = opq.fp8_quantize(torch.randn((M, K), device=DEV, generator=g).to(torch.bfloat16))
+    wc, ws = opq.fp8_quantize(torch.randn((N, K), device=DEV, generator=g).to(torch.bfloat16), 128)
+    clean = opq.fp8_linear(xc, xs, wc, ws, act=act)
+    xn, wn, xi = xc.view(torch.uint8).clone(), wc.view(torch.uint8).clone(), xs.clone()
+    xn[M // 2, 5] = 0x7F
+    wn[N // 3, 7] = 0xFF
+    xi[0, M - 1] = math.inf                                   # sums of +-inf: inf, NaN below
+    y = opq.fp8_linear(xn.view(F8), xi, wn.view(F8), ws, act=act)
+    hit = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    hit[M // 2], hit[:, N // 3], hit[M - 1] = True, True, True
+    assert bool(torch.isnan(y[M // 2]).all()) and bool(torch.isnan(y[:, N // 3]).all())
+    assert not bool(torch.isfinite(y[M - 1]).any())
+    assert torch.equal(y[~hit], clean[~hit])
